@@ -434,6 +434,123 @@ TRA_API tra_status hybrid_attention_prefill(const tra_shape* shape, const tra_hy
                                             float softmax_scale, uint16_t* out, float* lse,
                                             int32_t* status_dev, void* stream);
 
+/*
+ * Evicting key / value cache (the method's pages have no counterpart: they fix the cache
+ * at the end of the prompt).  A paged INT8 cache in which every (sequence, KV head) keeps
+ * its own tokens: the ones with the most accumulated attention weight, the sum over query
+ * heads and queries of the softmax probabilities a key has received.
+ * attention_weight_sums gives the prompt's weights (they also serve hybrid_select_tokens
+ * as its importance), paged_cache_fill stores a prompt, paged_attention_decode attends,
+ * adds the weights of its step and appends, paged_cache_evict shrinks the rows.
+ *
+ * attention_weight_sums -- for every key position j and KV head g
+ *   weights[j][g] = sum over the group's query heads h and the window's queries i >= j of
+ *                   exp(softmax_scale * q_ih . k_jg - lse[h][i]),
+ * the window being the last min(T, n_queries) queries of each sequence (n_queries = 0:
+ * all).  q, k: device bf16 as in quantize_qkv_tiles; weights: device float [ntok][Hkv],
+ * all written; lse: device float [Hq][ntok], natural logarithms: with lse_given != 0 it
+ * is read (the lse a prefill wrote; a row that is not finite adds nothing), otherwise the
+ * window's rows are computed from q and k (dense causal) and written, and the other rows
+ * are left as they were.  Products of bf16 inputs are summed in fp32, as are the weights,
+ * in a fixed order: the same call gives the same bits.  status_dev as in the prefill.
+ */
+TRA_API tra_status attention_weight_sums(const tra_shape* shape, const uint16_t* q, const uint16_t* k,
+                                         int32_t n_queries, float softmax_scale, float* lse,
+                                         int32_t lse_given, float* weights, int32_t* status_dev,
+                                         void* stream);
+
+/* device status word bits of the evicting cache */
+#define TRA_DEV_CACHE_FULL 0x8   /* a row has no free page for a step's full tail or an eviction's pages */
+#define TRA_DEV_BAD_CACHE 0x10   /* a page number or a row state out of range */
+
+/*
+ * The cache: B rows of Hkv heads.  A row holds n_pages pages of 64 tokens per head and a
+ * bf16 tail of 0 to 63 tokens, in order; state[b] = {n_pages, tail_len, seen, 0}, where
+ * `seen` counts every token the row was ever given.  A row with n_pages < 0 is idle:
+ * every call leaves it as it is.  table[b][g][i] is the page of head g's tokens
+ * 64 i .. 64 i + 63; its entries from n_pages on are the row's free pages.  All cap
+ * entries must be different numbers in [0, n_pool), over all rows and heads.
+ * A page is 64 x d codes (two's complement, row = token) of K and of V, each with one
+ * scale, by the INT8 rule above: s = fl32(amax / 127) over the page.  weight and pos
+ * (position in the sequence) are per token in the row's order, the tail behind the pages;
+ * entries behind the last token mean nothing and are left as they were.
+ * All device memory, caller-owned, 16-byte aligned.
+ */
+typedef struct {
+  int32_t B, Hq, Hkv, d;    /* Hq / Hkv <= 8; d 64 or 128 */
+  int32_t cap;              /* page table entries of a row and head */
+  int32_t n_pool;           /* pages in k8 / v8 / sk / sv */
+  int8_t* k8; int8_t* v8;   /* [n_pool][64][d] */
+  float* sk; float* sv;     /* [n_pool] */
+  int32_t* table;           /* [B][Hkv][cap] */
+  int32_t* state;           /* [B][4] */
+  float* weight;            /* [B][Hkv][(cap + 1) * 64] */
+  int32_t* pos;             /* [B][Hkv][(cap + 1) * 64] */
+  uint16_t* k_tail;         /* bf16 [B][Hkv][64][d] */
+  uint16_t* v_tail;
+} tra_paged_cache;
+
+/* Workspace bytes the three calls below need for this cache (sizes only are read; any
+ * content will do); 0 for an invalid one.  Calls that may run at the same time need a
+ * workspace each. */
+TRA_API size_t tra_paged_workspace_bytes(const tra_paged_cache* cache);
+
+/*
+ * paged_cache_fill -- a prompt's K and V into the cache: row b takes sequence b of
+ * `shape` (same B, Hq, Hkv, d).  The last T % 64 tokens become the tail; of the
+ * nb = floor(T / 64) * 64 before it the row keeps n = min(nb / 64, keep) pages per head: the
+ * tokens among the last `recent` of the sequence (the latest of them, if they are more
+ * than 64 n), then those of largest weight, equal weights going to the earlier position;
+ * stored by ascending position.  weights: device float [ntok][Hkv] (finite), or NULL: the
+ * latest 64 n tokens are kept and their weights start at zero.  k, v: device bf16
+ * [ntok][Hkv][d], finite.  Writes the pages and scales of table[b][g][0 .. n), the tail,
+ * weight, pos and state.  1 <= keep <= cap; recent >= 0.
+ */
+TRA_API tra_status paged_cache_fill(const tra_paged_cache* cache, const tra_shape* shape,
+                                    const uint16_t* k, const uint16_t* v, const float* weights,
+                                    int32_t keep, int32_t recent, void* workspace,
+                                    size_t workspace_bytes, int32_t* status_dev, void* stream);
+
+/*
+ * paged_attention_decode -- one token per row: every query head attends to its KV head's
+ * pages (K = s * code, V = s * code), tail and the new token; one softmax per head with
+ * queries in bf16, scores and statistics in fp32.  out bf16 [B][Hq][d].  Then
+ *   weight[b][g][i] += the sum of the group's probabilities of token i (the new token's
+ *   starts from zero), pos of the new token = seen, the token is appended to the tail and
+ *   seen grows by one; a tail of 64 tokens is quantised into page table[b][g][n_pages] and
+ *   becomes empty.
+ * q bf16 [B][Hq][d]; k_new, v_new bf16 [B][Hkv][d].  state_out, weight_out: where the new
+ * state and the weights of the row's tokens are written, or NULL for in place: a step
+ * that writes elsewhere can be repeated or dropped (a rejected draft token), since
+ * what it writes to the tail, to pos and to the free page lies behind the old state's
+ * tokens.  state_out and weight_out are the cache's own arrays or do not overlap them.
+ * A row whose tail would fill with no free page left sets TRA_DEV_CACHE_FULL, keeps its
+ * state and leaves its output, tail and weights untouched.
+ */
+TRA_API tra_status paged_attention_decode(const tra_paged_cache* cache, const uint16_t* q,
+                                          const uint16_t* k_new, const uint16_t* v_new,
+                                          float softmax_scale, uint16_t* out, int32_t* state_out,
+                                          float* weight_out, void* workspace, size_t workspace_bytes,
+                                          int32_t* status_dev, void* stream);
+
+/*
+ * paged_cache_evict -- every row of more than `keep` pages is cut to `keep` pages: of the
+ * page tokens, those among the row's last `recent` tokens (tail included; the latest, if they
+ * are more than 64 keep), then those of largest weight, equal weights going to the earlier
+ * token; in order.  A survivor's value fl32(s * code) is quantised again with its new
+ * page's scale.  The new pages are the row's free pages table[b][g][n_pages ..
+ * n_pages + keep), which move to the front of the table: {n .. n + keep - 1, 0 .. n - 1,
+ * n + keep ..}; the old pages are free afterwards and their contents unchanged.  weight and
+ * pos move with their tokens; the tail stays.  Shorter rows keep what they hold.
+ * state_out, table_out, weight_out, pos_out: where the row's new state is written (rows
+ * that stay are copied), or all NULL for in place.  A row with fewer than `keep` free
+ * pages sets TRA_DEV_CACHE_FULL and stays as it is.  1 <= keep <= cap; recent >= 0.
+ */
+TRA_API tra_status paged_cache_evict(const tra_paged_cache* cache, int32_t keep, int32_t recent,
+                                     int32_t* state_out, int32_t* table_out, float* weight_out,
+                                     int32_t* pos_out, void* workspace, size_t workspace_bytes,
+                                     int32_t* status_dev, void* stream);
+
 /* Complete-tile counts of one head's boundary pair over a batch (TriAttention
  * abstract: candidate boundary pairs are weighed by complete-tile execution costs):
  * n8 = sum over every sequence's q-tiles qt of min(qt + 1, b1), n4 = the sum of

@@ -17,5 +17,6 @@ from ._lib import (  # noqa: F401
     LISTS_PREFILL, LISTS_DECODE_CACHE, FMT_Q8, FMT_Q4, FMT_K8, FMT_K4, FMT_V8, FMT_V4, FMT_Q4X, FMT_K4X,
     DEV_TIMEOUT, DEV_TAIL_FULL, DEV_BAD_LIST, tra_selftest_bounded_wait, boundary_tile_counts,
     allocate_boundaries, prefill_cost_model, fit_prefill_cost_model, Hybrid, hybrid_select_tokens, hybrid_attention_decode,
-    hybrid_attention_prefill,
+    hybrid_attention_prefill, attention_weight_sums, PagedCache, paged_cache_fill,
+    paged_attention_decode, paged_cache_evict, DEV_CACHE_FULL, DEV_BAD_CACHE,
 )

@@ -25,6 +25,7 @@ FMT_Q8, FMT_Q4, FMT_K8, FMT_K4, FMT_V8, FMT_V4 = 0x1, 0x2, 0x4, 0x8, 0x10, 0x20
 FMT_Q4X, FMT_K4X = 0x40, 0x80
 FMT_Q8F, FMT_K8F = 0x100, 0x200
 DEV_TIMEOUT, DEV_TAIL_FULL, DEV_BAD_LIST = 0x1, 0x2, 0x4
+DEV_CACHE_FULL, DEV_BAD_CACHE = 0x8, 0x10
 STATUS = {0: "TRA_OK", 1: "TRA_ERR_INVALID", 2: "TRA_ERR_UNSUPPORTED", 3: "TRA_ERR_BUFFER",
           4: "TRA_ERR_CUDA", 5: "TRA_ERR_TIMEOUT"}
 
@@ -51,6 +52,12 @@ class _Hybrid(ctypes.Structure):
     _fields_ = [("window", ctypes.c_int32), ("cap", ctypes.c_int32)] + \
                [(n, ctypes.c_void_p) for n in
                 ("sel_count", "sel_pos", "sel_mask", "k_sel", "v_sel", "k_win", "v_win")]
+
+
+class _PagedCache(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("B", "Hq", "Hkv", "d", "cap", "n_pool")] + \
+               [(n, ctypes.c_void_p) for n in
+                ("k8", "v8", "sk", "sv", "table", "state", "weight", "pos", "k_tail", "v_tail")]
 
 
 class _QTiles(ctypes.Structure):
@@ -95,6 +102,11 @@ def load():
         "hybrid_select_tokens": ([P, P, ctypes.c_double, P, P, P, P], I32),
         "hybrid_attention_decode": ([P, P, P, P, P, P, P, P, P, I32, F, P, P, SZ, P, P], I32),
         "hybrid_attention_prefill": ([P, P, P, P, P, P, P, P, F, P, P, P, P], I32),
+        "attention_weight_sums": ([P, P, P, I32, F, P, I32, P, P, P], I32),
+        "tra_paged_workspace_bytes": ([P], SZ),
+        "paged_cache_fill": ([P, P, P, P, P, I32, I32, P, SZ, P, P], I32),
+        "paged_attention_decode": ([P, P, P, P, F, P, P, P, P, SZ, P, P], I32),
+        "paged_cache_evict": ([P, I32, I32, P, P, P, P, P, SZ, P, P], I32),
     }
     for name, (args, res) in sig.items():
         fn = getattr(lib, name)
@@ -142,6 +154,7 @@ class Shape:
         self.cu_dev = torch.as_tensor(self.cu_host).to(device) if device is not None else None
         self.B = len(self.cu_host) - 1
         self.Hq, self.Hkv, self.d = Hq, Hkv, d
+        self._status = None
         self._c = _Shape(self.B, Hq, Hkv, d,
                          self.cu_dev.data_ptr() if self.cu_dev is not None else 16,
                          self.cu_host.ctypes.data)
@@ -149,6 +162,13 @@ class Shape:
     @property
     def c(self):
         return ctypes.byref(self._c)
+
+    @property
+    def status(self):
+        """Device status word (TRA_DEV_* bits) of the calls on this shape that are given none."""
+        if self._status is None:
+            self._status = torch.zeros(1, dtype=torch.int32, device=self.cu_dev.device)
+        return self._status
 
     @property
     def ntok(self) -> int:
@@ -347,6 +367,130 @@ def hybrid_attention_prefill(shape: Shape, hy: Hybrid, q, k, v, kv: QTiles, k_mi
         shape.c, hy.c, _ptr(q), _ptr(k), _ptr(v), kv.c, _ptr(k_mix), _ptr(v_mix),
         float(softmax_scale), _ptr(out), _ptr(lse) if lse is not None else None, _ptr(status),
         _stream(stream)))
+
+
+def _expect(name, t, dtype, shape, device):
+    """t: a contiguous tensor of this dtype, shape and device (TraError otherwise)."""
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or tuple(t.shape) != shape \
+            or not t.is_contiguous() or t.device != device:
+        raise TraError(1, f"{name} must be a contiguous {dtype} tensor of shape {shape} on {device}")
+
+
+def _launch_device(t):
+    """t's device, which has to be the current one: the kernels start there."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TraError(1, "a tensor on a CUDA device is required")
+    if t.get_device() != torch.cuda.current_device():
+        raise TraError(1, f"the tensors are on {t.device}, which is not the current device")
+    return t.device
+
+
+def attention_weight_sums(shape: Shape, q, k, weights, lse, *, n_queries: int = 0, softmax_scale,
+                          lse_given: bool = False, status=None, stream=None):
+    """Accumulated attention weight of every key (float32 weights [ntok, Hkv]) over the last
+    n_queries queries of each sequence (0: all).  lse [Hq, ntok]: read if lse_given, else the
+    window's rows are computed and written.  status: device int32 (default: shape.status)."""
+    dev = _launch_device(q)
+    n, hq, hkv, d = shape.ntok, shape.Hq, shape.Hkv, shape.d
+    _expect("q", q, torch.bfloat16, (n, hq, d), dev)
+    _expect("k", k, torch.bfloat16, (n, hkv, d), dev)
+    _expect("weights", weights, torch.float32, (n, hkv), dev)
+    _expect("lse", lse, torch.float32, (hq, n), dev)
+    _check(load().attention_weight_sums(
+        shape.c, _ptr(q), _ptr(k), int(n_queries), float(softmax_scale), _ptr(lse), int(bool(lse_given)),
+        _ptr(weights), _ptr(shape.status if status is None else status), _stream(stream)))
+
+
+class PagedCache:
+    """The evicting key / value cache (include/tra.h, tra_paged_cache): B rows of up to `cap`
+    pages of 64 INT8 tokens per KV head and a bf16 tail.  `tensors`: the cache's own arrays by
+    name (all of them), otherwise they are allocated, with the pages of a pool of n_pool =
+    B * Hkv * cap dealt out in order and every row idle until paged_cache_fill."""
+
+    NAMES = ("k8", "v8", "sk", "sv", "table", "state", "weight", "pos", "k_tail", "v_tail")
+
+    def __init__(self, B: int, Hq: int, Hkv: int, d: int, cap: int, tensors=None, device="cuda"):
+        if min(B, Hq, Hkv, d, cap) < 1:
+            raise TraError(1, "B, Hq, Hkv, d and cap must be >= 1")
+        self.B, self.Hq, self.Hkv, self.d, self.cap = B, Hq, Hkv, d, cap
+        n_pool = B * Hkv * cap if tensors is None else int(tensors["k8"].shape[0])
+        spec = {"k8": ((n_pool, TILE, d), torch.int8), "sk": ((n_pool,), torch.float32),
+                "table": ((B, Hkv, cap), torch.int32), "state": ((B, 4), torch.int32),
+                "weight": ((B, Hkv, (cap + 1) * TILE), torch.float32),
+                "pos": ((B, Hkv, (cap + 1) * TILE), torch.int32),
+                "k_tail": ((B, Hkv, TILE, d), torch.bfloat16)}
+        spec |= {"v8": spec["k8"], "sv": spec["sk"], "v_tail": spec["k_tail"]}
+        if tensors is None:
+            self.t = {n: torch.zeros(spec[n][0], dtype=spec[n][1], device=device) for n in self.NAMES}
+            self.t["table"].copy_(torch.arange(n_pool, dtype=torch.int32).view(B, Hkv, cap))
+            self.t["state"][:, 0] = -1
+        else:
+            self.t = {n: tensors[n] for n in self.NAMES}
+            for n in self.NAMES:
+                _expect(n, self.t[n], spec[n][1], spec[n][0], self.t["k8"].device)
+        self.n_pool, self.device = n_pool, self.t["k8"].device
+        self._c = _PagedCache(B, Hq, Hkv, d, cap, n_pool, *[self.t[n].data_ptr() for n in self.NAMES])
+        nbytes = int(load().tra_paged_workspace_bytes(self.c))
+        if nbytes == 0:
+            raise TraError(1, load().tra_last_error().decode())
+        self.workspace = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
+        self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
+
+    def __getitem__(self, k):
+        return self.t[k]
+
+    @property
+    def c(self):
+        return ctypes.byref(self._c)
+
+    def _tail_args(self, stream):
+        return (_ptr(self.workspace), self.workspace.numel(), _ptr(self.status), _stream(stream))
+
+    def _outs(self, **outs):
+        for n, t in outs.items():
+            if t is not None:
+                own = self.t[n]
+                _expect(n + "_out", t, own.dtype, tuple(own.shape), self.device)
+
+
+def paged_cache_fill(cache: PagedCache, shape: Shape, k, v, *, keep: int, recent: int = 0, weights=None,
+                     stream=None):
+    """The prompts of `shape` into the cache's rows, each cut to the `keep` pages of its last
+    `recent` tokens and those of largest weight (float32 [ntok, Hkv]; None: the latest)."""
+    dev = _launch_device(k)
+    n = shape.ntok
+    _expect("cache", cache.t["k8"], torch.int8, (cache.n_pool, TILE, cache.d), dev)
+    _expect("k", k, torch.bfloat16, (n, cache.Hkv, cache.d), dev)
+    _expect("v", v, torch.bfloat16, (n, cache.Hkv, cache.d), dev)
+    if weights is not None:
+        _expect("weights", weights, torch.float32, (n, cache.Hkv), dev)
+    _check(load().paged_cache_fill(cache.c, shape.c, _ptr(k), _ptr(v), _ptr(weights), int(keep), int(recent),
+                                   *cache._tail_args(stream)))
+
+
+def paged_attention_decode(cache: PagedCache, q, k_new, v_new, out, *, softmax_scale, state_out=None,
+                           weight_out=None, stream=None):
+    """One token per row: attention over the row, its probabilities added to the weights, and the
+    append (include/tra.h).  state_out, weight_out: where those go instead of the cache's own."""
+    dev = _launch_device(q)
+    B, d = cache.B, cache.d
+    _expect("q", q, torch.bfloat16, (B, cache.Hq, d), dev)
+    _expect("k_new", k_new, torch.bfloat16, (B, cache.Hkv, d), dev)
+    _expect("v_new", v_new, torch.bfloat16, (B, cache.Hkv, d), dev)
+    _expect("out", out, torch.bfloat16, (B, cache.Hq, d), cache.device)
+    cache._outs(state=state_out, weight=weight_out)
+    _check(load().paged_attention_decode(cache.c, _ptr(q), _ptr(k_new), _ptr(v_new), float(softmax_scale), _ptr(out),
+                                         _ptr(state_out), _ptr(weight_out), *cache._tail_args(stream)))
+
+
+def paged_cache_evict(cache: PagedCache, *, keep: int, recent: int = 0, state_out=None, table_out=None,
+                      weight_out=None, pos_out=None, stream=None):
+    """Every row of more than `keep` pages is cut to that many (include/tra.h).  The outputs: all
+    four or none (in place)."""
+    _launch_device(cache.t["k8"])
+    cache._outs(state=state_out, table=table_out, weight=weight_out, pos=pos_out)
+    _check(load().paged_cache_evict(cache.c, int(keep), int(recent), _ptr(state_out), _ptr(table_out),
+                                    _ptr(weight_out), _ptr(pos_out), *cache._tail_args(stream)))
 
 
 def boundary_tile_counts(shape: Shape, b1: int, b2: int):

@@ -775,6 +775,209 @@ tra_status hybrid_attention_prefill(const tra_shape* shape, const tra_hybrid* hy
   return ok();
 }
 
+// ------------------------------------------------------------------ weight sums, evicting cache
+tra_status attention_weight_sums(const tra_shape* shape, const uint16_t* q, const uint16_t* k,
+                                 int32_t n_queries, float softmax_scale, float* lse,
+                                 int32_t lse_given, float* weights, int32_t* status_dev,
+                                 void* stream) {
+  const CallRange range("tra::attention_weight_sums");
+  int64_t nt = 0, ntok = 0, nt_max = 0;
+  tra_status st = check_shape(shape, &nt, &ntok, &nt_max);
+  if (st != TRA_OK) return st;
+  if (n_queries < 0) return fail(TRA_ERR_INVALID, "n_queries must be >= 0 (got %d)", n_queries);
+  if (!q || !k || !lse || !weights || !status_dev)
+    return fail(TRA_ERR_INVALID, "q, k, lse, weights and status are required");
+  if (!aligned16(q) || !aligned16(k) || !aligned16(lse) || !aligned16(weights))
+    return fail(TRA_ERR_INVALID, "q/k/lse/weights must be 16-byte aligned");
+  if (!(softmax_scale > 0.0f) || !std::isfinite(softmax_scale))
+    return fail(TRA_ERR_INVALID, "softmax_scale must be positive and finite");
+  if (nt == 0) return ok();
+  tra::WeightParams p{};
+  p.cu = shape->cu_seqlens_dev;
+  p.B = shape->B;
+  p.Hq = shape->Hq;
+  p.Hkv = shape->Hkv;
+  p.d = shape->d;
+  p.n_queries = n_queries;
+  // work units (128 rows) of both passes and their 128 x 128 tiles
+  const int64_t grp = shape->Hq / shape->Hkv;
+  int64_t q_tiles = 0, k_tiles = 0;  // most of a sequence
+  for (int b = 0; b < shape->B; ++b) {
+    const int64_t T = shape->cu_seqlens_host[b + 1] - shape->cu_seqlens_host[b];
+    const int64_t W = n_queries > 0 ? std::min<int64_t>(T, n_queries) : T;
+    const int64_t nk = (T + 127) / 128, nq = (W + 127) / 128;
+    // key tiles that the queries see, of full tiles: nk for the last query tile, one less each
+    const int64_t tiles = nq * nk - nq * (nq - 1) / 2;
+    q_tiles = std::max(q_tiles, nq);
+    k_tiles = std::max(k_tiles, nk);
+    p.lse_steps += tiles * shape->Hq;
+    p.lse_longest = std::max<long long>(p.lse_longest, nk);
+    p.sum_steps += tiles * shape->Hq;
+    p.sum_longest = std::max<long long>(p.sum_longest, nq * grp);
+  }
+  p.lse_units = q_tiles * shape->B * shape->Hq;
+  p.sum_units = k_tiles * shape->B * shape->Hkv;
+  p.ntok = ntok;
+  p.scale_log2 = softmax_scale * 1.4426950408889634f;
+  p.lse_given = lse_given != 0;
+  p.lse = lse;
+  p.weights = weights;
+  p.status = status_dev;
+  tra::WeightMaps m;
+  memset(&m, 0, sizeof m);
+  if (!map_bf16(&m.q, q, shape->d, shape->Hq, ntok, 128) || !map_bf16(&m.k, k, shape->d, shape->Hkv, ntok, 128))
+    return fail(TRA_ERR_CUDA, "cuTensorMapEncodeTiled failed (driver entry point or arguments)");
+  cudaError_t e = tra::launch_weight_sums(p, m, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "weight sums launch");
+  return ok();
+}
+
+// Sizes of a paged cache (its pointers are checked by check_paged).
+static tra_status check_paged_sizes(const tra_paged_cache* c) {
+  if (!c) return fail(TRA_ERR_INVALID, "cache is NULL");
+  if (c->B < 1 || c->Hq < 1 || c->Hkv < 1) return fail(TRA_ERR_INVALID, "B, Hq and Hkv must be >= 1");
+  if (c->Hq % c->Hkv) return fail(TRA_ERR_INVALID, "Hq (%d) must be a multiple of Hkv (%d)", c->Hq, c->Hkv);
+  if (c->Hq / c->Hkv > 8) return fail(TRA_ERR_UNSUPPORTED, "the paged cache supports Hq/Hkv <= 8");
+  if (c->Hq > TRA_MAX_HEADS || c->B > 65535) return fail(TRA_ERR_UNSUPPORTED, "Hq > %d or B > 65535", TRA_MAX_HEADS);
+  if (c->d != 64 && c->d != 128) return fail(TRA_ERR_UNSUPPORTED, "head dim %d (64 or 128 supported)", c->d);
+  if (c->cap < 1 || c->n_pool < 1) return fail(TRA_ERR_INVALID, "cap and n_pool must be >= 1");
+  if (c->cap >= 1 << 24 || c->n_pool >= 1 << 25) return fail(TRA_ERR_UNSUPPORTED, "cap >= 2^24 or n_pool >= 2^25");
+  return TRA_OK;
+}
+
+static tra_status check_paged(const tra_paged_cache* c, const void* workspace, size_t workspace_bytes,
+                              const int32_t* status_dev, tra::PagedLayout* lay) {
+  tra_status st = check_paged_sizes(c);
+  if (st != TRA_OK) return st;
+  const void* const ptrs[10] = {c->k8, c->v8, c->sk, c->sv, c->table, c->state, c->weight, c->pos, c->k_tail, c->v_tail};
+  for (const void* x : ptrs) {
+    if (!x) return fail(TRA_ERR_INVALID, "an array of the cache is NULL");
+    if (!aligned16(x)) return fail(TRA_ERR_INVALID, "the cache's arrays must be 16-byte aligned");
+  }
+  if (!workspace || !status_dev) return fail(TRA_ERR_INVALID, "workspace and status are required");
+  if (!aligned16(workspace)) return fail(TRA_ERR_INVALID, "workspace must be 16-byte aligned");
+  *lay = tra::paged_layout(*c);
+  if (workspace_bytes < lay->total) return fail(TRA_ERR_BUFFER, "workspace needs %zu bytes", lay->total);
+  return TRA_OK;
+}
+
+size_t tra_paged_workspace_bytes(const tra_paged_cache* cache) {
+  if (check_paged_sizes(cache) != TRA_OK) return 0;
+  return tra::paged_layout(*cache).total;
+}
+
+tra_status paged_cache_fill(const tra_paged_cache* cache, const tra_shape* shape, const uint16_t* k,
+                            const uint16_t* v, const float* weights, int32_t keep, int32_t recent,
+                            void* workspace, size_t workspace_bytes, int32_t* status_dev, void* stream) {
+  const CallRange range("tra::paged_cache_fill");
+  tra::PagedLayout lay;
+  tra_status st = check_paged(cache, workspace, workspace_bytes, status_dev, &lay);
+  if (st != TRA_OK) return st;
+  st = check_shape(shape, nullptr, nullptr, nullptr);
+  if (st != TRA_OK) return st;
+  if (shape->B != cache->B || shape->Hq != cache->Hq || shape->Hkv != cache->Hkv || shape->d != cache->d)
+    return fail(TRA_ERR_INVALID, "shape and cache differ in B, Hq, Hkv or d");
+  if (!k || !v || !aligned16(k) || !aligned16(v)) return fail(TRA_ERR_INVALID, "k and v are required, 16-byte aligned");
+  if (reinterpret_cast<uintptr_t>(weights) & 3u) return fail(TRA_ERR_INVALID, "weights misaligned");
+  if (keep < 1 || keep > cache->cap) return fail(TRA_ERR_INVALID, "keep must lie in [1, %d] (got %d)", cache->cap, keep);
+  if (recent < 0) return fail(TRA_ERR_INVALID, "recent must be >= 0");
+  uint8_t* const ws = reinterpret_cast<uint8_t*>(workspace);
+  tra::PagedCutParams p{};
+  p.c = *cache;
+  p.keep = keep;
+  p.recent = recent;
+  for (int b = 0; b < shape->B; ++b)
+    p.nmax = std::max(p.nmax, shape->cu_seqlens_host[b + 1] - shape->cu_seqlens_host[b]);
+  p.cu = shape->cu_seqlens_dev;
+  p.k = k;
+  p.v = v;
+  p.imp = weights;
+  p.state_out = cache->state;
+  p.table_out = cache->table;
+  p.weight_out = cache->weight;
+  p.pos_out = cache->pos;
+  p.status = status_dev;
+  p.ws_state = reinterpret_cast<int4*>(ws + lay.state);
+  p.ws_src = reinterpret_cast<int32_t*>(ws + lay.src);
+  p.ws_dst = reinterpret_cast<int32_t*>(ws + lay.dst);
+  cudaError_t e = tra::launch_paged_fill(p, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "paged fill launch");
+  return ok();
+}
+
+tra_status paged_attention_decode(const tra_paged_cache* cache, const uint16_t* q, const uint16_t* k_new,
+                                  const uint16_t* v_new, float softmax_scale, uint16_t* out,
+                                  int32_t* state_out, float* weight_out, void* workspace,
+                                  size_t workspace_bytes, int32_t* status_dev, void* stream) {
+  const CallRange range("tra::paged_attention_decode");
+  tra::PagedLayout lay;
+  tra_status st = check_paged(cache, workspace, workspace_bytes, status_dev, &lay);
+  if (st != TRA_OK) return st;
+  if (!q || !k_new || !v_new || !out) return fail(TRA_ERR_INVALID, "q, k_new, v_new and out are required");
+  if (!aligned16(q) || !aligned16(k_new) || !aligned16(v_new) || !aligned16(out) ||
+      !aligned16(state_out) || !aligned16(weight_out))
+    return fail(TRA_ERR_INVALID, "q/k_new/v_new/out/state_out/weight_out must be 16-byte aligned");
+  if (!(softmax_scale > 0.0f) || !std::isfinite(softmax_scale))
+    return fail(TRA_ERR_INVALID, "softmax_scale must be positive and finite");
+  uint8_t* const ws = reinterpret_cast<uint8_t*>(workspace);
+  tra::PagedStepParams p{};
+  p.c = *cache;
+  p.q = q;
+  p.k_new = k_new;
+  p.v_new = v_new;
+  p.scale_log2 = softmax_scale * 1.4426950408889634f;
+  p.out = out;
+  p.state_out = state_out ? state_out : cache->state;
+  p.weight_out = weight_out ? weight_out : cache->weight;
+  p.status = status_dev;
+  p.ws_state = reinterpret_cast<int4*>(ws + lay.state);
+  p.part_ml = reinterpret_cast<float*>(ws + lay.ml);
+  p.part_o = reinterpret_cast<float*>(ws + lay.o);
+  p.scores = reinterpret_cast<float*>(ws + lay.scores);
+  tra::PagedMaps m;
+  memset(&m, 0, sizeof m);
+  const int64_t rows = (int64_t)cache->n_pool * TRA_TILE;
+  if (!map_i8(&m.k8, cache->k8, cache->d, rows, TRA_TILE) || !map_i8(&m.v8, cache->v8, cache->d, rows, TRA_TILE))
+    return fail(TRA_ERR_CUDA, "cuTensorMapEncodeTiled failed (driver entry point or arguments)");
+  cudaError_t e = tra::launch_paged_step(p, m, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "paged decode launch");
+  return ok();
+}
+
+tra_status paged_cache_evict(const tra_paged_cache* cache, int32_t keep, int32_t recent,
+                             int32_t* state_out, int32_t* table_out, float* weight_out,
+                             int32_t* pos_out, void* workspace, size_t workspace_bytes,
+                             int32_t* status_dev, void* stream) {
+  const CallRange range("tra::paged_cache_evict");
+  tra::PagedLayout lay;
+  tra_status st = check_paged(cache, workspace, workspace_bytes, status_dev, &lay);
+  if (st != TRA_OK) return st;
+  const int given = (state_out != nullptr) + (table_out != nullptr) + (weight_out != nullptr) + (pos_out != nullptr);
+  if (given != 0 && given != 4)
+    return fail(TRA_ERR_INVALID, "state_out, table_out, weight_out and pos_out are given together or not at all");
+  if (!aligned16(state_out) || !aligned16(table_out) || !aligned16(weight_out) || !aligned16(pos_out))
+    return fail(TRA_ERR_INVALID, "state_out/table_out/weight_out/pos_out must be 16-byte aligned");
+  if (keep < 1 || keep > cache->cap) return fail(TRA_ERR_INVALID, "keep must lie in [1, %d] (got %d)", cache->cap, keep);
+  if (recent < 0) return fail(TRA_ERR_INVALID, "recent must be >= 0");
+  uint8_t* const ws = reinterpret_cast<uint8_t*>(workspace);
+  tra::PagedCutParams p{};
+  p.c = *cache;
+  p.keep = keep;
+  p.recent = recent;
+  p.nmax = (int)std::min<int64_t>((int64_t)cache->cap * TRA_TILE, 1 << 30);
+  p.state_out = given ? state_out : cache->state;
+  p.table_out = given ? table_out : cache->table;
+  p.weight_out = given ? weight_out : cache->weight;
+  p.pos_out = given ? pos_out : cache->pos;
+  p.status = status_dev;
+  p.ws_state = reinterpret_cast<int4*>(ws + lay.state);
+  p.ws_src = reinterpret_cast<int32_t*>(ws + lay.src);
+  p.ws_dst = reinterpret_cast<int32_t*>(ws + lay.dst);
+  cudaError_t e = tra::launch_paged_evict(p, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "paged evict launch");
+  return ok();
+}
+
 tra_status tra_boundary_tile_counts(const tra_shape* shape, int32_t b1, int32_t b2, int64_t* n8,
                                     int64_t* n4) {
   tra_status st = check_shape(shape, nullptr, nullptr, nullptr);

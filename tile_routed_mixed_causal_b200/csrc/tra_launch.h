@@ -176,6 +176,83 @@ struct HybridMixParams {
 
 cudaError_t launch_hybrid_mix(const HybridMixParams& p, cudaStream_t s);
 
+// ------------------------------------------------------------ weight sums of a prompt
+struct WeightParams {
+  const int32_t* cu;
+  int B, Hq, Hkv, d, n_queries;
+  long long ntok;
+  float scale_log2;      // softmax_scale * log2(e)
+  int lse_given;
+  float* lse;            // [Hq][ntok]
+  float* weights;        // [ntok][Hkv]
+  int32_t* status;
+  // work units of the two passes (grid sizes), and their 128 x 128 tiles: all, of the longest
+  long long lse_units, lse_steps, lse_longest;
+  long long sum_units, sum_steps, sum_longest;
+};
+
+struct WeightMaps {
+  CUtensorMap q, k;      // bf16 (d, H, ntok), boxes of 64 channels x 128 tokens
+};
+
+cudaError_t launch_weight_sums(const WeightParams& p, const WeightMaps& m, cudaStream_t s);
+
+// ------------------------------------------------------------ evicting cache
+// One decode step.  Workspace: row states as the step found them, partial (m, l, o) of
+// every piece of a row that a CTA took, and the scores of every token (log2 domain).
+struct PagedStepParams {
+  tra_paged_cache c;
+  const uint16_t* q;
+  const uint16_t* k_new;
+  const uint16_t* v_new;
+  float scale_log2;
+  uint16_t* out;
+  int32_t* state_out;
+  float* weight_out;
+  int32_t* status;
+  int4* ws_state;        // [B]
+  float* part_ml;        // [pieces][grp][2]
+  float* part_o;         // [pieces][grp][d]
+  float* scores;         // [B][Hkv][(cap + 1) * 64][paged_score_stride(grp)]
+};
+
+struct PagedMaps {
+  CUtensorMap k8, v8;    // codes as rows of d bytes, boxes of one page
+};
+
+// Fill (src = prompt) and evict (src = the cache): select the survivors of every row, then
+// quantise them page by page.  Workspace: row states, the survivors' source rows and the
+// destination pages.
+struct PagedCutParams {
+  tra_paged_cache c;
+  int keep, recent;
+  int nmax;              // most tokens of a row that are chosen among
+  // fill
+  const int32_t* cu;
+  const uint16_t* k;
+  const uint16_t* v;
+  const float* imp;      // [ntok][Hkv] or null
+  // evict
+  int32_t* state_out;
+  int32_t* table_out;
+  float* weight_out;
+  int32_t* pos_out;
+  int32_t* status;
+  int4* ws_state;        // [B] {pages after the call, tail, seen, 1 if the row is cut or filled}
+  int32_t* ws_src;       // [B][Hkv][keep * 64] token of the sequence, or page * 64 + slot
+  int32_t* ws_dst;       // [B][Hkv][keep] destination page, -1: none
+};
+
+struct PagedLayout {     // byte offsets in the workspace
+  size_t state, ml, o, scores, src, dst, total;
+};
+PagedLayout paged_layout(const tra_paged_cache& c);
+// floats per token in the score array: the group's heads, an even number above one
+__host__ __device__ inline int paged_score_stride(int grp) { return grp == 1 ? 1 : (grp + 1) & ~1; }
+cudaError_t launch_paged_step(const PagedStepParams& p, const PagedMaps& m, cudaStream_t s);
+cudaError_t launch_paged_fill(const PagedCutParams& p, cudaStream_t s);
+cudaError_t launch_paged_evict(const PagedCutParams& p, cudaStream_t s);
+
 int decode_splits(int B, int Hkv);
 cudaError_t launch_wait_selftest(int32_t* status, uint64_t limit_ns, cudaStream_t s);
 cudaError_t launch_decode(const DecodeParams& p, const DecodeMaps& m, cudaStream_t s);

@@ -1,0 +1,467 @@
+// weights.cu -- accumulated attention weight of a prompt's keys (the importance that
+// hybrid_select_tokens and the evicting cache take): for key j and KV head g
+//   w[j][g] = sum over the query heads h of g and the window's queries i >= j of
+//             exp(scale q_ih . k_jg - lse[h][i]),
+// and, where the caller has none, lse[h][i] = log sum_{j <= i} exp(scale q_ih . k_jg).
+//
+// Both are one kernel with the roles of queries and keys exchanged.  A work unit is 128
+// rows (the M of one tcgen05 MMA, TMEM lanes) against a stream of 128-column tiles:
+//   sums:  rows = 128 keys of one KV head, columns = queries of all heads of its group;
+//          a thread owns a key and adds exp2(s c - lse2[column]), no exchange at all;
+//   lse:   rows = 128 queries of one head, columns = keys; a thread owns a query and keeps
+//          its running maximum and sum.
+// The scores live in TMEM and registers only.  Per element the kernel needs one product
+// column of the tensor cores (d multiply-adds, 4096 per SM and cycle) and one exponential
+// (16 per SM and cycle), so for d <= 128 the exponentials bound it.
+// Roles (384 threads, two CTAs per SM): warp 0 copies tiles (TMA), warp 1 issues the MMAs,
+// warps 2 and 3 stage the columns' normalisers (sums only), warps 4-7 and 8-11 take the
+// even and the odd tiles, one S block of TMEM each.
+// Sums run in fp32: within a tile over four chains, tile sums with a compensated add, so
+// that the error does not grow with the number of tiles.
+// Where there are few units a cluster of up to 8 CTAs shares one (every C-th tile each)
+// and joins the partial rows over distributed shared memory in rank order: the same call
+// gives the same bits.
+#include "tra_device.cuh"
+#include "tra_launch.h"
+
+namespace tra {
+namespace {
+
+constexpr int kWThreads = 384;
+constexpr int kRows = 128;   // rows of a unit, columns of a tile
+constexpr int kColSlots = 4;
+constexpr uint32_t kWTmemCols = 256;  // two S blocks of 128 fp32 columns
+// log2 units by which a row's scores may pass its reference maximum before the sum is
+// rescaled: the sum stays below 2^16 * 2^31
+constexpr float kLseSlack = 16.0f;
+
+template <int D>
+struct WCfg {
+  static constexpr int kTileBytes = kRows * D * 2;
+  static constexpr int kStages = D == 128 ? 2 : 3;
+  static constexpr int kSlabs = D / 64;
+  static constexpr int kOffA = 0;
+  static constexpr int kOffB = kTileBytes;
+  static constexpr int kOffCol = kOffB + kStages * kTileBytes;     // [kColSlots][128] float
+  static constexpr int kOffFlag = kOffCol + kColSlots * kRows * 4;  // [kColSlots][2] int
+  static constexpr int kOffRed = kOffFlag + kColSlots * 2 * 4;      // [2][128] float2
+  static constexpr int kOffBar = kOffRed + 2 * kRows * 8;
+  static constexpr int kNumBars = 1 + 2 * kStages + 4 + 2 * kColSlots + 1;
+  static constexpr int kOffMisc = kOffBar + kNumBars * 8;
+  static constexpr int kUsed = kOffMisc + 32 + 1024;
+  // at least 80 KB, so that no more than two CTAs share an SM: their S blocks fill its TMEM
+  static constexpr int kSmem = kUsed > 80 * 1024 ? kUsed : 80 * 1024;
+  static_assert(2 * (kSmem + 1024) <= 228 * 1024, "two CTAs per SM");
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// this CTA's shared address `a` in CTA `rank` of the cluster
+__device__ __forceinline__ float2 ld_cluster_f2(uint32_t a, uint32_t rank) {
+  uint32_t m;
+  float2 v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(m) : "r"(a), "r"(rank));
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(m) : "memory");
+  return v;
+}
+
+__device__ __forceinline__ void mma_bf16_e(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc,
+                                           uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// One unit and the tiles of its stream that this CTA takes.
+template <bool LSE>
+struct WUnit {
+  bool valid;
+  int b, head;       // head: query head (lse), KV head (sums)
+  int seq0, T, wq0;  // sequence start, length, first query of the window
+  int r0;            // first row (query or key) within the sequence
+  int ncol, c0;      // column tiles per head, the first of them
+  int steps;         // tiles of the stream (all CTAs of the cluster)
+
+  __device__ __forceinline__ void init(const WeightParams& p, long long id) {
+    const int H = LSE ? p.Hq : p.Hkv;
+    head = (int)(id % H);
+    b = (int)((id / H) % p.B);
+    const int t = (int)(id / ((long long)H * p.B));
+    seq0 = __ldg(p.cu + b);
+    T = __ldg(p.cu + b + 1) - seq0;
+    const int W = p.n_queries > 0 ? min(T, p.n_queries) : T;
+    wq0 = T - W;
+    if (LSE) {  // query tiles count from the window's first query; the longest rows first
+      const int nq = (W + kRows - 1) / kRows;
+      valid = t < nq;
+      r0 = wq0 + (nq - 1 - t) * kRows;
+      c0 = 0;
+      ncol = valid ? min(r0 + kRows, T) - 1 : 0;
+      ncol = ncol / kRows + 1;  // key tiles 0 .. that of the last row
+      steps = valid ? ncol : 0;
+    } else {  // key tiles in order: the first are seen by the most queries
+      valid = t * kRows < T;
+      r0 = t * kRows;
+      const int nq = (W + kRows - 1) / kRows;
+      c0 = r0 > wq0 ? (r0 - wq0) / kRows : 0;  // earlier tiles end before the first key
+      ncol = nq - c0;
+      steps = valid ? ncol * (p.Hq / p.Hkv) : 0;
+    }
+  }
+  // step u: query head and first query (sums), or first key (lse) of the column tile
+  __device__ __forceinline__ void column(const WeightParams& p, int u, int& h, int& x0) const {
+    if (LSE) {
+      h = head / (p.Hq / p.Hkv);
+      x0 = u * kRows;
+    } else {
+      h = head * (p.Hq / p.Hkv) + u / ncol;
+      x0 = wq0 + (c0 + u % ncol) * kRows;
+    }
+  }
+};
+
+template <int D, bool LSE>
+__global__ void __launch_bounds__(kWThreads, 2)
+    weight_kernel(const __grid_constant__ WeightParams p, const __grid_constant__ WeightMaps m) {
+  using C = WCfg<D>;
+  extern __shared__ uint8_t wsm_raw[];
+  const uint32_t base = (smem_u32(wsm_raw) + 1023u) & ~1023u;
+  uint8_t* const gbase = wsm_raw + (base - smem_u32(wsm_raw));
+  const uint32_t rank = cluster_rank(), nrank = cluster_size();
+  WUnit<LSE> x;
+  x.init(p, blockIdx.x / nrank);
+  if (!x.valid) return;  // the whole cluster leaves
+  const int nsteps = (x.steps - (int)rank + (int)nrank - 1) / (int)nrank;  // this CTA's, may be 0
+
+  const uint32_t bars = base + C::kOffBar;
+  const uint32_t bar_a = bars;
+  auto bar_bfull = [&](int s) { return bars + (1 + s) * 8; };
+  auto bar_bfree = [&](int s) { return bars + (1 + C::kStages + s) * 8; };
+  constexpr int kSB = 1 + 2 * C::kStages;
+  auto bar_sfull = [&](int w) { return bars + (kSB + w) * 8; };
+  auto bar_sfree = [&](int w) { return bars + (kSB + 2 + w) * 8; };
+  auto bar_cfull = [&](int s) { return bars + (kSB + 4 + s) * 8; };
+  auto bar_cfree = [&](int s) { return bars + (kSB + 4 + kColSlots + s) * 8; };
+  const uint32_t bar_done = bars + (kSB + 4 + 2 * kColSlots) * 8;
+  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(gbase + C::kOffMisc);
+  volatile int* const err = reinterpret_cast<volatile int*>(gbase + C::kOffMisc + 16);
+  float* const col = reinterpret_cast<float*>(gbase + C::kOffCol);
+  volatile int* const flag = reinterpret_cast<volatile int*>(gbase + C::kOffFlag);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    mbar_init(bar_a, 1);
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(bar_bfull(s), 1);
+      mbar_init(bar_bfree(s), 1);
+    }
+    for (int w = 0; w < 2; ++w) {
+      mbar_init(bar_sfull(w), 1);
+      mbar_init(bar_sfree(w), 4);
+    }
+    for (int s = 0; s < kColSlots; ++s) {
+      mbar_init(bar_cfull(s), 64);
+      mbar_init(bar_cfree(s), 4);
+    }
+    mbar_init(bar_done, 1);
+    *err = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), kWTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  auto wwait = [&](uint32_t bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, err));
+  };
+
+  // a row's result: sums (total, -), lse (reference maximum, sum)
+  float2 part = make_float2(LSE ? -INFINITY : 0.0f, 0.0f);
+
+  if (warp == 0) {
+    // ---------------------------------------------------------------- TMA
+    const CUtensorMap* const ma = LSE ? &m.q : &m.k;
+    const CUtensorMap* const mb = LSE ? &m.k : &m.q;
+    mbar_arrive_expect_tx_e(bar_a, C::kTileBytes);
+    for (int sl = 0; sl < C::kSlabs; ++sl)
+      tma_load_3d_e(base + C::kOffA + sl * kRows * 128, ma, bar_a, sl * 64, x.head, x.seq0 + x.r0);
+    int n = 0;
+    for (; n < nsteps; ++n) {
+      const int s = n % C::kStages, use = n / C::kStages;
+      if (use > 0 && !wwait(bar_bfree(s), (use - 1) & 1)) break;
+      int h, x0;
+      x.column(p, (int)rank + n * (int)nrank, h, x0);
+      mbar_arrive_expect_tx_e(bar_bfull(s), C::kTileBytes);
+      for (int sl = 0; sl < C::kSlabs; ++sl)
+        tma_load_3d_e(base + C::kOffB + s * C::kTileBytes + sl * kRows * 128, mb, bar_bfull(s), sl * 64, h,
+                      x.seq0 + x0);
+    }
+    // every copy lands before the CTA can leave (only this warp arrives on these barriers)
+    if (nsteps == 0 || *err) {
+      mbar_wait_drain(bar_a, 0);
+      for (int s = 0; s < C::kStages && s < n; ++s)
+        mbar_wait_drain(bar_bfull(s), (uint32_t)(((n - 1 - s) / C::kStages) & 1));
+    }
+  } else if (warp == 1) {
+    // ---------------------------------------------------------------- MMA
+    constexpr uint32_t kId = instr_desc(1, 1, 0, 0, kRows, 128);
+    const uint64_t dA = smem_desc(base + C::kOffA, 16, 1024, kSwz128);
+    bool ok = nsteps > 0 && wwait(bar_a, 0);
+    for (int n = 0; ok && n < nsteps; ++n) {
+      const int s = n % C::kStages, w = n & 1;
+      // S block w last held tile n - 2; its warps have read it into registers
+      if (n >= 2 && !wwait(bar_sfree(w), ((n >> 1) - 1) & 1)) break;
+      if (!wwait(bar_bfull(s), (n / C::kStages) & 1)) break;
+      tc_fence_after();
+      const uint64_t dB = smem_desc(base + C::kOffB + s * C::kTileBytes, 16, 1024, kSwz128);
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk)  // 16 channels: 32 bytes within a 64-channel slab of 16 KB
+        mma_bf16_e(tmem + w * kRows, dA + (kk >> 2) * 1024 + (kk & 3) * 2, dB + (kk >> 2) * 1024 + (kk & 3) * 2,
+                   kId, kk > 0 ? 1u : 0u);
+      mma_commit_e(bar_bfree(s));
+      mma_commit_e(bar_sfull(w));
+    }
+    // every MMA is complete before TMEM is released
+    mma_commit_e(bar_done);
+    mbar_wait_drain(bar_done, 0);
+    __syncwarp();
+  } else if (warp < 4) {
+    // ---------------------------------------------------------------- column normalisers
+    if (!LSE) {
+      const int c = (warp - 2) * 64 + lane;  // and c + 32
+      for (int n = 0; n < nsteps; ++n) {
+        const int s = n % kColSlots, use = n / kColSlots;
+        if (use > 0 && !wwait(bar_cfree(s), (use - 1) & 1)) break;
+        int h, x0;
+        x.column(p, (int)rank + n * (int)nrank, h, x0);
+        const float* const src = p.lse + (long long)h * p.ntok + x.seq0;
+        bool odd = false;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int i = x0 + c + 32 * k;
+          const float z = i < x.T ? src[i] : INFINITY;
+          const bool fin = isfinite(z);  // a row that is not finite adds nothing
+          odd |= !fin;
+          col[s * kRows + c + 32 * k] = fin ? z * -1.4426950408889634f : -INFINITY;
+        }
+        odd = __any_sync(0xffffffffu, odd);
+        if (lane == 0) flag[s * 2 + warp - 2] = odd;
+        __syncwarp();
+        mbar_arrive(bar_cfull(s));
+      }
+    }
+  } else {
+    // ---------------------------------------------------------------- softmax warps
+    const int w = (warp - 4) >> 2;                    // tile parity, S block
+    const int r = (warp & 3) * 32 + lane;             // row = TMEM lane
+    const int row = x.r0 + r;                         // query or key position
+    const uint32_t tS = tmem + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)(w * kRows);
+    const float c1 = p.scale_log2;
+    const float2 c2 = make_float2(c1, c1);
+    float total = 0.0f, comp = 0.0f;                  // sums: compensated total
+    float mref = -INFINITY, l = 0.0f;                 // lse
+    for (int n = w; n < nsteps; n += 2) {
+      const int cs = n % kColSlots;
+      int h, x0;
+      x.column(p, (int)rank + n * (int)nrank, h, x0);
+      if (!LSE && !mbar_wait(bar_cfull(cs), (n / kColSlots) & 1, err)) break;
+      if (!mbar_wait(bar_sfull(w), (n >> 1) & 1, err)) break;
+      __syncwarp();
+      tc_fence_after();
+      if (LSE) {
+        // keys behind the last row of the sequence are behind every valid row, too
+        const bool masked = x0 + kRows - 1 > x.r0;
+        const int nchunk = min(kRows, x.T - x0 + 31) >> 5;
+#pragma unroll 1
+        for (int ch = 0; ch < nchunk; ++ch) {
+          uint32_t sr[32];
+          tmem_ld32(tS + 32 * ch, sr);
+          tmem_wait_ld();
+          tmem_reg_fence(sr);
+          if (masked) {
+            const int lim = row - (x0 + 32 * ch);  // columns 0 .. lim are visible
+#pragma unroll
+            for (int k = 0; k < 32; ++k) sr[k] = k <= lim ? sr[k] : 0xFF800000u;
+          }
+          float mx[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) mx[k] = __uint_as_float(sr[k]);
+#pragma unroll
+          for (int k = 4; k < 32; ++k) mx[k & 3] = fmaxf(mx[k & 3], __uint_as_float(sr[k]));
+          const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c1;
+          if (mt > mref + kLseSlack || (mref == -INFINITY && mt > mref)) {
+            l *= ex2(mref - mt);  // mref = -inf gives 0
+            mref = mt;
+          }
+          const float nm = mref == -INFINITY ? 0.0f : -mref;
+          const float2 nm2 = make_float2(nm, nm);
+          float2 a[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+#pragma unroll
+          for (int k = 0; k < 32; k += 2) {
+            const float2 e = __ffma2_rn(make_float2(__uint_as_float(sr[k]), __uint_as_float(sr[k + 1])), c2, nm2);
+            a[(k >> 1) & 1] = __fadd2_rn(a[(k >> 1) & 1], make_float2(ex2(e.x), ex2(e.y)));
+          }
+          const float2 s2 = __fadd2_rn(a[0], a[1]);
+          l += s2.x + s2.y;
+        }
+      } else {
+        // queries before the key, past the window's end or without a finite lse add
+        // nothing; where a tile has such columns they are selected away one by one, since
+        // a score there may be anything
+        const bool masked = x0 < x.r0 + kRows - 1 || flag[cs * 2] || flag[cs * 2 + 1];
+        const int nchunk = min(kRows, x.T - x0 + 31) >> 5;
+        const float4* const nl = reinterpret_cast<const float4*>(col + cs * kRows);
+        float2 a[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+#pragma unroll 1
+        for (int ch = 0; ch < nchunk; ++ch) {
+          uint32_t sr[32];
+          tmem_ld32(tS + 32 * ch, sr);
+          tmem_wait_ld();
+          tmem_reg_fence(sr);
+          if (!masked) {
+#pragma unroll
+            for (int k = 0; k < 32; k += 4) {
+              const float4 z = nl[8 * ch + k / 4];
+              const float2 e0 = __ffma2_rn(make_float2(__uint_as_float(sr[k]), __uint_as_float(sr[k + 1])), c2,
+                                           make_float2(z.x, z.y));
+              const float2 e1 = __ffma2_rn(make_float2(__uint_as_float(sr[k + 2]), __uint_as_float(sr[k + 3])), c2,
+                                           make_float2(z.z, z.w));
+              a[0] = __fadd2_rn(a[0], make_float2(ex2(e0.x), ex2(e0.y)));
+              a[1] = __fadd2_rn(a[1], make_float2(ex2(e1.x), ex2(e1.y)));
+            }
+          } else {
+            const int lim = row - (x0 + 32 * ch);  // columns from lim on see the key
+#pragma unroll
+            for (int k = 0; k < 32; k += 4) {
+              const float4 z = nl[8 * ch + k / 4];
+              const float zz[4] = {z.x, z.y, z.z, z.w};
+              float e[4];
+#pragma unroll
+              for (int y = 0; y < 4; ++y) {
+                e[y] = ex2(fmaf(__uint_as_float(sr[k + y]), c1, zz[y]));
+                if (k + y < lim || zz[y] == -INFINITY) e[y] = 0.0f;
+              }
+              a[0] = __fadd2_rn(a[0], make_float2(e[0], e[1]));
+              a[1] = __fadd2_rn(a[1], make_float2(e[2], e[3]));
+            }
+          }
+        }
+        const float2 s2 = __fadd2_rn(a[0], a[1]);
+        // compensated add: comp carries what the total could not hold
+        const float y = __fsub_rn(s2.x + s2.y, comp);
+        const float t = __fadd_rn(total, y);
+        comp = __fsub_rn(__fsub_rn(t, total), y);
+        total = t;
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(bar_sfree(w));
+        if (!LSE) mbar_arrive(bar_cfree(cs));
+      }
+    }
+    part = LSE ? make_float2(mref, l) : make_float2(total, 0.0f);
+    reinterpret_cast<float2*>(gbase + C::kOffRed)[w * kRows + r] = part;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, kWTmemCols);  // before the wait for other CTAs
+  if (threadIdx.x == 0 && *err) atomicOr(p.status, *err);
+
+  // join the CTAs' rows, even tiles then odd ones of each rank
+  if (nrank > 1) cluster_sync();
+  if (rank == 0 && threadIdx.x < kRows && x.r0 + (int)threadIdx.x < x.T) {
+    const uint32_t red = base + C::kOffRed + threadIdx.x * 8;
+    const int row = x.r0 + threadIdx.x;
+    float mm = -INFINITY, acc = 0.0f;
+    if (LSE)
+      for (uint32_t k = 0; k < nrank; ++k)
+        for (uint32_t w = 0; w < 2; ++w) mm = fmaxf(mm, ld_cluster_f2(red + w * kRows * 8, k).x);
+    for (uint32_t k = 0; k < nrank; ++k)
+      for (uint32_t w = 0; w < 2; ++w) {
+        const float2 v = ld_cluster_f2(red + w * kRows * 8, k);
+        if (LSE) acc += v.x == -INFINITY ? 0.0f : v.y * ex2(v.x - mm);
+        else acc += v.x;
+      }
+    if (LSE)
+      p.lse[(long long)x.head * p.ntok + x.seq0 + row] = (mm + log2f(acc)) * 0.69314718055994531f;
+    else
+      p.weights[(long long)(x.seq0 + row) * p.Hkv + x.head] = acc;
+  }
+  __syncwarp();
+  if (nrank > 1) cluster_sync();  // a CTA's rows stay until rank 0 has read them
+}
+
+// CTAs per unit: as few as bring the longest unit near the mean load of the grid's 296
+// places (two per SM), so that a short stream of units still fills the GPU.
+int cluster_for(long long total, long long longest) {
+  const long long mean = total / 296 > 4 ? total / 296 : 4;
+  int c = 1;
+  while (c < 8 && (longest + c - 1) / c > mean) c *= 2;
+  return c;
+}
+
+template <int D, bool LSE>
+cudaError_t launch_weight_pass(const WeightParams& p, const WeightMaps& m, long long units, int cluster,
+                               cudaStream_t s) {
+  using C = WCfg<D>;
+  cudaError_t e = cudaFuncSetAttribute(weight_kernel<D, LSE>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  if (e != cudaSuccess) return e;
+  if (units * cluster > 0x7FFFFFFFll) return cudaErrorInvalidConfiguration;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(units * cluster));
+  cfg.blockDim = dim3(kWThreads);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = (unsigned)cluster;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, weight_kernel<D, LSE>, p, m);
+}
+
+template <int D>
+cudaError_t launch_weight_d(const WeightParams& p, const WeightMaps& m, cudaStream_t s) {
+  if (!p.lse_given) {
+    cudaError_t e = launch_weight_pass<D, true>(p, m, p.lse_units, cluster_for(p.lse_steps, p.lse_longest), s);
+    if (e != cudaSuccess) return e;
+  }
+  return launch_weight_pass<D, false>(p, m, p.sum_units, cluster_for(p.sum_steps, p.sum_longest), s);
+}
+
+}  // namespace
+
+cudaError_t launch_weight_sums(const WeightParams& p, const WeightMaps& m, cudaStream_t s) {
+  return p.d == 128 ? launch_weight_d<128>(p, m, s) : launch_weight_d<64>(p, m, s);
+}
+
+}  // namespace tra
