@@ -2,33 +2,36 @@
 // row's survivors by accumulated weight and write them as pages of 64 quantised tokens.
 //
 // Selection, one CTA of 1024 threads per (sequence, KV head): the weights' ordered bits are
-// staged once in shared memory; a radix select (three digits of 11, 11 and 10 bits) finds
-// the want-th largest, and one ascending pass of 4096 tokens at a time writes the survivors'
-// source rows, weights and positions at their ranks, ties taken in order.  Every chunk is
-// read by the whole block before any of it is written, and a survivor never moves up, so a
-// row can be cut in place.  Bound by latency: some ten block-wide steps.
+// staged once in shared memory, protected tokens as the largest; a radix select (three digits
+// of 11, 11 and 10 bits) finds the last key that survives, and one ascending pass writes the
+// survivors' indices at their ranks, ties taken in order.  Bound by latency: a dozen
+// block-wide steps, so it writes nothing but the indices.
 //
-// Pages, one CTA of 256 threads per (page, KV head, sequence): 64 gathered rows of K and of
-// V are held in registers while their maxima are reduced, then written as codes: one read
-// and one write of what survives, bound by memory.  (Survivors are single rows of d values
-// anywhere in the source, 128 to 256 bytes each: every access is whole sectors.)
+// Pages, one CTA per (up to four pages, K or V, KV head, sequence): 64 gathered rows are held in
+// registers while their maximum is reduced, then written as codes, the next page's rows
+// already on their way; the K part moves the tokens' weights, the V part their positions.
+// One read and one write of what survives: bound by memory.  (Survivors are single rows of
+// d values anywhere in the source, 64 to 256 bytes each: every access is whole sectors.)
+//
+// A row that is cut in place gets its weights and positions through the workspace and a
+// third kernel, since pages are written in any order.
+#include <cuda_fp16.h>
+
 #include "paged_device.cuh"
 
 namespace tra {
 namespace {
 
 constexpr int kSelThreads = 1024;
-constexpr int kChunkTok = 4 * kSelThreads;
-constexpr int kStageMax = 48 * 1024;  // keys held in shared memory (192 KB)
+constexpr int kSpan = 48 * 1024;      // tokens ranked at a time; keys that fit shared memory (192 KB)
+constexpr int kSpanChunks = kSpan / (4 * kSelThreads);
+constexpr uint32_t kKeepKey = 0xFFFFFFFFu;  // above every finite weight's key
 
-// Monotone map of a float's bits to unsigned order (-0 as +0), and back.
+// Monotone map of a float's bits to unsigned order (-0 as +0); finite values map above 0.
 __device__ __forceinline__ uint32_t order_of(float f) {
   uint32_t u = __float_as_uint(f);
   if (u == 0x80000000u) u = 0u;
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
-}
-__device__ __forceinline__ float value_of(uint32_t o) {
-  return __uint_as_float((o & 0x80000000u) ? o ^ 0x80000000u : ~o);
 }
 
 // Exclusive sum over the block; the total in `all`.  tmp: 33 words, and two barriers.
@@ -60,206 +63,213 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* tmp, uint32
 
 template <bool FILL>
 __global__ void __launch_bounds__(kSelThreads) paged_select_kernel(const PagedCutParams p, int stage) {
-  extern __shared__ uint32_t keys[];
+  extern __shared__ __align__(16) uint32_t keys[];
   __shared__ uint32_t hist[2048];
   __shared__ uint32_t tmp[33];
+  __shared__ uint2 warp_sum[kSpanChunks * 32 + 1];
   __shared__ uint32_t s_bin, s_want;
-  const int g = blockIdx.x, b = blockIdx.y, t = threadIdx.x;
+  const int g = blockIdx.x, b = blockIdx.y, t = threadIdx.x, warp = t >> 5, lane = t & 31;
   const tra_paged_cache& c = p.c;
   const int row = b * c.Hkv + g;
   const long long row64 = (long long)row * (c.cap + 1) * kTile;
-  int32_t* const table = c.table + (long long)row * c.cap;
-  int32_t* const table_out = p.table_out + (long long)row * c.cap;
 
-  // tokens to choose among (body), tail behind them, pages after the call (n)
-  int body, tail, n, from = 0, total = 0;
+  // tokens to choose among (body), pages after the call (n), all tokens (total)
+  int body, n, from = 0, total = 0;
   if (FILL) {
     from = __ldg(p.cu + b);
     total = __ldg(p.cu + b + 1) - from;
     body = total / kTile * kTile;
-    tail = total - body;
     n = min(body / kTile, p.keep);
-    if (g == 0 && t == 0) p.ws_state[b] = make_int4(n, tail, total, 1);
+    if (g == 0 && t == 0) p.ws_state[b] = make_int4(n, total - body, total, 1);
   } else {
     const int4 st = reinterpret_cast<const int4*>(c.state)[b];
     const PagedRow kind = paged_row(st, c.cap);
     const bool full = kind == kRowOk && st.x > p.keep && st.x > c.cap - p.keep;
     const bool cut = kind == kRowOk && st.x > p.keep && !full;
     if (g == 0 && t == 0) {
-      p.ws_state[b] = make_int4(p.keep, st.y, st.z, cut);
+      p.ws_state[b] = make_int4(st.x, st.y, kind == kRowOk, cut);
       if (kind == kRowBad) atomicOr(p.status, TRA_DEV_BAD_CACHE);
       if (full) atomicOr(p.status, TRA_DEV_CACHE_FULL);
     }
-    if (!cut) {  // the row stays: into the output arrays as it is
-      if (table_out != table) {
-        for (int i = t; i < c.cap; i += kSelThreads) table_out[i] = table[i];
-        const int m = kind == kRowOk ? st.x * kTile + st.y : 0;
-        for (int i = t; i < m; i += kSelThreads) {
-          p.weight_out[row64 + i] = c.weight[row64 + i];
-          p.pos_out[row64 + i] = c.pos[row64 + i];
-        }
-      }
-      return;
-    }
+    if (!cut) return;
     body = st.x * kTile;
-    tail = st.y;
     n = p.keep;
-    total = body + tail;
+    total = body + st.y;
   }
   const int m = n * kTile;
-  // tokens from `first` on are kept; `want` more among those before it
-  const bool ranked = !FILL || p.imp != nullptr;
-  int first = ranked ? max(total - p.recent, body - m) : body - m;
-  first = min(first, body);
-  const int want = m - (body - first);
-
-  auto weight_at = [&](int j) -> float {
-    if (FILL) return p.imp ? p.imp[(long long)(from + j) * c.Hkv + g] : 0.0f;
-    return c.weight[row64 + j];
+  // the tokens from `first` on survive whatever their weight
+  int first = !FILL || p.imp ? min(max(total - p.recent, body - m), body) : body - m;
+  if (m == body) first = 0;
+  int32_t* const out = p.ws_src + (long long)row * c.cap * kTile;
+  int32_t* const out_row = FILL ? nullptr : p.ws_row + (long long)row * c.cap * kTile;
+  // evict: the rows of the codes that hold tokens j .., a page at a time
+  const int32_t* const table = c.table + (long long)row * c.cap;
+  auto page_row = [&](int j) -> int {
+    if (FILL || j >= body) return 0;
+    const int page = table[j / kTile];
+    if (page < 0 || page >= c.n_pool) {
+      atomicOr(p.status, TRA_DEV_BAD_CACHE);
+      return j % kTile;
+    }
+    return page * kTile + j % kTile;
   };
-  const bool staged = first <= stage;
-  auto key_at = [&](int j) -> uint32_t { return staged ? keys[j] : order_of(weight_at(j)); };
-
-  // the tail's weights and positions, before anything of the row is overwritten
-  float tail_w = 0.0f;
-  int tail_p = 0;
-  if (t < tail) {
-    tail_w = weight_at(body + t);
-    tail_p = FILL ? body + t : c.pos[row64 + body + t];
+  if (body - first == m) {
+    for (int i = t; i < m; i += kSelThreads) {
+      out[i] = first + i;
+      if (!FILL) out_row[i] = page_row(first + i);
+    }
+    return;
   }
 
-  uint32_t kth = 0;       // survivors before `first`: keys above kth,
-  uint32_t ties = 0;      // and the first `ties` equal to it
-  const bool all = want >= first;
-  if (!all && want > 0) {
-    if (staged) {
-      if (FILL) {
+  const float* const w_row = FILL ? p.imp + (long long)from * c.Hkv + g : c.weight + row64;
+  const long long w_step = FILL ? c.Hkv : 1;
+  auto load_key = [&](int j) -> uint32_t { return j < first ? order_of(w_row[j * w_step]) : kKeepKey; };
+  const bool staged = body <= stage;  // (a multiple of 64)
+  auto key4 = [&](int j) -> uint4 {   // of tokens j .. j + 3, j a multiple of 4
+    if (j >= body) return make_uint4(0, 0, 0, 0);
+    if (staged) return *reinterpret_cast<const uint4*>(keys + j);
+    return make_uint4(load_key(j), load_key(j + 1), load_key(j + 2), load_key(j + 3));
+  };
+  hist[t] = 0;
+  hist[t + kSelThreads] = 0;
+  __syncthreads();
+  if (staged) {
+    if (FILL) {
+#pragma unroll 8
+      for (int j = t; j < body; j += kSelThreads) {
+        const uint32_t k = load_key(j);
+        keys[j] = k;
+        atomicAdd(&hist[k >> 21], 1u);
+      }
+    } else {  // a row's weights start on a 256-byte boundary
 #pragma unroll 4
-        for (int j = t; j < first; j += kSelThreads) keys[j] = order_of(weight_at(j));
-      } else {  // the row starts on a 256-byte boundary
-        const float4* const w4 = reinterpret_cast<const float4*>(c.weight + row64);
-#pragma unroll 2
-        for (int j = t; j < (first + 3) / 4; j += kSelThreads) {
-          const float4 v = w4[j];
-          const uint32_t o[4] = {order_of(v.x), order_of(v.y), order_of(v.z), order_of(v.w)};
-          if (4 * j + 3 < first) {
-            *reinterpret_cast<uint4*>(keys + 4 * j) = make_uint4(o[0], o[1], o[2], o[3]);
-          } else {
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              if (4 * j + k < first) keys[4 * j + k] = o[k];
-          }
+      for (int j = 4 * t; j < body; j += 4 * kSelThreads) {
+        const float4 v = *reinterpret_cast<const float4*>(w_row + j);
+        uint4 k = make_uint4(order_of(v.x), order_of(v.y), order_of(v.z), order_of(v.w));
+        if (j + 3 >= first) {
+          if (j >= first) k.x = kKeepKey;
+          if (j + 1 >= first) k.y = kKeepKey;
+          if (j + 2 >= first) k.z = kKeepKey;
+          k.w = kKeepKey;
         }
+        *reinterpret_cast<uint4*>(keys + j) = k;
+        atomicAdd(&hist[k.x >> 21], 1u);
+        atomicAdd(&hist[k.y >> 21], 1u);
+        atomicAdd(&hist[k.z >> 21], 1u);
+        atomicAdd(&hist[k.w >> 21], 1u);
       }
     }
-    uint32_t need = (uint32_t)want;
-#pragma unroll 1
-    for (int pass = 0; pass < 3; ++pass) {
-      const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
-      const int bits = pass == 2 ? 10 : 11;
+  } else {
+    for (int j = t; j < body; j += kSelThreads) atomicAdd(&hist[load_key(j) >> 21], 1u);
+  }
+
+  // ---- the m-th largest key, and how many of the keys equal to it survive
+  uint32_t kth = 0, need = (uint32_t)m;
+#pragma unroll
+  for (int pass = 0; pass < 3; ++pass) {
+    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+    const int bits = pass == 2 ? 10 : 11;
+    if (pass > 0) {
       hist[t] = 0;
       hist[t + kSelThreads] = 0;
       __syncthreads();
-      for (int j = t; j < first; j += kSelThreads) {
-        const uint32_t k = key_at(j);
-        if (pass == 0 || (k >> (shift + bits)) == kth)
-          atomicAdd(&hist[(k >> shift) & ((1u << bits) - 1u)], 1u);
-      }
-      __syncthreads();
-      // from the top: thread t has bins 2047 - 2t and 2046 - 2t
-      const uint32_t h0 = hist[2047 - 2 * t], h1 = hist[2046 - 2 * t];
-      uint32_t sum;
-      const uint32_t above = block_scan(h0 + h1, tmp, sum);
-      if (above < need && need <= above + h0 + h1) {
-        const bool second = need > above + h0;
-        s_bin = 2047 - 2 * t - second;
-        s_want = need - above - (second ? h0 : 0);
-      }
-      __syncthreads();
-      kth = (kth << bits) | s_bin;
-      need = s_want;
-    }
-    ties = need;
-  }
-
-  // ---- ascending pass
-  int32_t* const src_out = p.ws_src + (long long)row * c.cap * kTile;
-  uint32_t gt_base = 0, eq_base = 0;
-  const bool chosen = !all && want > 0;
-  // nothing before `first` survives when want = 0
-  const int begin = want > 0 ? 0 : first / kChunkTok * kChunkTok;
-  for (int c0 = begin; c0 < body; c0 += kChunkTok) {
-    const int j0 = c0 + 4 * t;
-    bool gt[4], eq[4];
-    float w[4];
-    int ps[4], src[4];
-    uint32_t cnt = 0;
-    const int page = (!FILL && j0 < body) ? table[j0 / kTile] : 0;
-    const bool bad_page = !FILL && (page < 0 || page >= c.n_pool);
-    if (bad_page) atomicOr(p.status, TRA_DEV_BAD_CACHE);
+      for (int j = 4 * t; j < body; j += 4 * kSelThreads) {
+        const uint4 k4 = key4(j);
+        const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int j = j0 + k;
-      const bool in = j < body, early = j < first;
-      const uint32_t key = in && early && chosen ? key_at(j) : 0u;
-      gt[k] = in && (!early || all || (chosen && key > kth));
-      eq[k] = in && early && chosen && key == kth;
-      cnt += (gt[k] ? 0x10000u : 0u) + (eq[k] ? 1u : 0u);
-      w[k] = 0.0f;
-      ps[k] = j;
-      src[k] = FILL ? j : (bad_page ? 0 : page) * kTile + j % kTile;
-      if (gt[k] || eq[k]) {
-        w[k] = early && chosen && staged ? value_of(key) : weight_at(j);
-        if (!FILL) ps[k] = c.pos[row64 + j];
+        for (int y = 0; y < 4; ++y)
+          if ((k[y] >> (shift + bits)) == kth) atomicAdd(&hist[(k[y] >> shift) & ((1u << bits) - 1u)], 1u);
       }
     }
-    // (a chunk holds at most 4096 of each kind: the two 16-bit halves cannot overflow)
+    __syncthreads();
+    // from the top: thread t has bins 2047 - 2t and 2046 - 2t
+    const uint32_t h0 = hist[2047 - 2 * t], h1 = hist[2046 - 2 * t];
     uint32_t sum;
-    const uint32_t pre = block_scan(cnt, tmp, sum);  // its barriers: all of the chunk is read
-    uint32_t gr = gt_base + (pre >> 16), er = eq_base + (pre & 0xFFFFu);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const uint32_t dst = gr + min(er, ties);
-      if (gt[k] || (eq[k] && er < ties)) {
-        src_out[dst] = src[k];
-        p.weight_out[row64 + dst] = w[k];
-        p.pos_out[row64 + dst] = ps[k];
-      }
-      gr += gt[k];
-      er += eq[k];
+    const uint32_t above = block_scan(h0 + h1, tmp, sum);
+    if (above < need && need <= above + h0 + h1) {
+      const bool second = need > above + h0;
+      s_bin = 2047 - 2 * t - second;
+      s_want = need - above - (second ? h0 : 0);
     }
-    gt_base += sum >> 16;
-    eq_base += sum & 0xFFFFu;
     __syncthreads();
+    kth = (kth << bits) | s_bin;
+    need = s_want;
   }
-  if (t < tail) {
-    p.weight_out[row64 + m + t] = tail_w;
-    p.pos_out[row64 + m + t] = tail_p;
-  }
+  const uint32_t ties = need;
 
-  // ---- destination pages; an evicted row's table turns by them
-  int32_t* const dst_out = p.ws_dst + (long long)row * c.cap;
-  const int d0 = FILL ? 0 : body / kTile;  // first destination entry
-  for (int i = t; i < n; i += kSelThreads) {
-    const int page = table[d0 + i];
-    const bool bad = page < 0 || page >= c.n_pool;
-    if (bad) atomicOr(p.status, TRA_DEV_BAD_CACHE);
-    dst_out[i] = bad ? -1 : page;
-  }
-  if (!FILL) {
-    __syncthreads();
-    const int old = d0;
-    // the old pages move up by n, the last ones first
-    for (int hi = old; hi > 0; hi -= kSelThreads) {
-      const int i = hi - 1 - t;
-      const int page = i >= 0 ? table[i] : 0;
-      __syncthreads();
-      if (i >= 0) table_out[n + i] = page;
-      __syncthreads();
+  // ---- ranks, a span at a time: per-warp counts of keys above and equal, their prefix over
+  // the span, then each survivor's index at its rank
+  uint32_t above0 = 0, equal0 = 0;
+  for (int s0 = 0; s0 < body; s0 += kSpan) {
+    const int chunks = (min(kSpan, body - s0) + 4 * kSelThreads - 1) / (4 * kSelThreads);
+    for (int i = 0; i < chunks; ++i) {
+      const uint4 k = key4(s0 + (i * kSelThreads + t) * 4);
+      const uint32_t a = (k.x > kth) + (k.y > kth) + (k.z > kth) + (k.w > kth);
+      const uint32_t e = (k.x == kth) + (k.y == kth) + (k.z == kth) + (k.w == kth);
+      const uint32_t both = __reduce_add_sync(0xffffffffu, a << 16 | e);
+      if (lane == 0) warp_sum[i * 32 + warp] = make_uint2(both >> 16, both & 0xFFFFu);
     }
-    for (int i = t; i < n; i += kSelThreads) table_out[i] = dst_out[i];
-    if (table_out != table)
-      for (int i = old + n + t; i < c.cap; i += kSelThreads) table_out[i] = table[i];
+    __syncthreads();
+    if (warp == 0) {  // exclusive prefix in place: lane l has entries l * chunks ..
+      uint2 own = make_uint2(0, 0);
+      for (int i = 0; i < chunks; ++i) {
+        const uint2 v = warp_sum[lane * chunks + i];
+        own.x += v.x;
+        own.y += v.y;
+      }
+      uint2 run = own;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t x = __shfl_up_sync(0xffffffffu, run.x, o), y = __shfl_up_sync(0xffffffffu, run.y, o);
+        if (lane >= o) {
+          run.x += x;
+          run.y += y;
+        }
+      }
+      if (lane == 31) warp_sum[kSpanChunks * 32] = run;
+      run.x -= own.x;
+      run.y -= own.y;
+      for (int i = 0; i < chunks; ++i) {
+        const uint2 v = warp_sum[lane * chunks + i];
+        warp_sum[lane * chunks + i] = run;
+        run.x += v.x;
+        run.y += v.y;
+      }
+    }
+    __syncthreads();
+    for (int i = 0; i < chunks; ++i) {
+      const int j = s0 + (i * kSelThreads + t) * 4;
+      const int prow = page_row(j);
+      const uint4 k4 = key4(j);
+      const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
+      uint32_t both = 0;
+#pragma unroll
+      for (int y = 0; y < 4; ++y) both += k[y] > kth ? 0x10000u : k[y] == kth ? 1u : 0u;
+      uint32_t pre = both;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t u = __shfl_up_sync(0xffffffffu, pre, o);
+        if (lane >= o) pre += u;
+      }
+      pre -= both;
+      const uint2 w = warp_sum[i * 32 + warp];
+      uint32_t a = above0 + w.x + (pre >> 16), e = equal0 + w.y + (pre & 0xFFFFu);
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        const bool gt = k[y] > kth, eq = k[y] == kth;
+        if (gt || (eq && e < ties)) {
+          const uint32_t at = a + min(e, ties);
+          out[at] = j + y;
+          if (!FILL) out_row[at] = prow + y;
+        }
+        a += gt;
+        e += eq;
+      }
+    }
+    const uint2 all = warp_sum[kSpanChunks * 32];
+    above0 += all.x;
+    equal0 += all.y;
+    __syncthreads();
   }
 }
 
@@ -282,127 +292,284 @@ __device__ __forceinline__ void floats16(uint4 v, float (&f)[16]) {
   }
 }
 
-// codes of fl32(s * code) for a new scale sn; ratio = s / sn
-__device__ __forceinline__ uint4 recode16(uint4 v, float s, float sn, float ratio) {
+// The largest and the smallest biased code seen so far, in 16-bit pairs.
+struct CodeRange {
+  uint32_t hi, lo;
+  __device__ __forceinline__ void reset() {
+    hi = 0u;
+    lo = 0x00FF00FFu;
+  }
+  __device__ __forceinline__ void add(uint4 v) {
+    const uint32_t w[4] = {v.x ^ 0x80808080u, v.y ^ 0x80808080u, v.z ^ 0x80808080u, v.w ^ 0x80808080u};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t even = w[i] & 0x00FF00FFu, odd = __byte_perm(w[i], 0u, 0x4341);
+      hi = __vimax3_u16x2(hi, even, odd);
+      lo = __vimin3_u16x2(lo, even, odd);
+    }
+  }
+  __device__ __forceinline__ float largest() const {  // |code|
+    const int h = max(hi & 0xFFFFu, hi >> 16), l = min(lo & 0xFFFFu, lo >> 16);
+    return (float)max(h - 128, 128 - l);
+  }
+};
+
+__device__ __noinline__ uint32_t code_exact(float s, float f, float sn) {
+  return (uint32_t)quant_code(__fmul_rn(s, f), sn, 127);
+}
+
+// recode16 where some values straddle a half: those by the definition.
+__device__ __noinline__ uint4 recode16_exact(uint4 v, float s, float sn, float fa, float fb) {
+  uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t o = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float f = __uint_as_float(__byte_perm(w[i] ^ 0x80808080u, 0x4B000000u, 0x7440 + j)) - 8388736.0f;
+      const float za = fmaf(f, fa, kRoundMagic), zb = fmaf(f, fb, kRoundMagic);
+      uint32_t c = __float_as_uint(za);
+      if (!(za == zb) || sn < kSmallScale) c = code_exact(s, f, sn);
+      o = j == 0 ? c & 0xFFu : __byte_perm(o, c, j == 1 ? 0x3240 : j == 2 ? 0x3410 : 0x4210);
+    }
+    w[i] = o;
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Codes of fl32(s * code) for the new scale sn; fa, fb: s / sn, above and below.
+__device__ __forceinline__ uint4 recode16(uint4 v, float s, float sn, float fa, float fb) {
   float f[16], z[16];
   floats16(v, f);
-  float far = 0.0f;
-  const float2 r2 = make_float2(ratio, ratio);
-#pragma unroll
-  for (int j = 0; j < 16; j += 2) {
-    const float2 x = make_float2(f[j], f[j + 1]);
-    const float2 zz = __ffma2_rn(x, r2, make_float2(kRoundMagic, kRoundMagic));
-    const float2 cn = __ffma2_rn(zz, make_float2(-1.0f, -1.0f), make_float2(kRoundMagic, kRoundMagic));
-    const float2 t = __ffma2_rn(x, r2, cn);
-    z[j] = zz.x;
-    z[j + 1] = zz.y;
-    far = fmaxf(far, fmaxf(fabsf(t.x), fabsf(t.y)));
-  }
-  if (far < kNearHalf && sn >= kSmallScale)
+  if (round_codes<16>(f, fa, fb, z) == 0.0f && sn >= kSmallScale)
     return make_uint4(low_bytes(z[0], z[1], z[2], z[3]), low_bytes(z[4], z[5], z[6], z[7]),
                       low_bytes(z[8], z[9], z[10], z[11]), low_bytes(z[12], z[13], z[14], z[15]));
-  uint32_t o[4] = {0, 0, 0, 0};
-#pragma unroll
-  for (int j = 0; j < 16; ++j)
-    o[j >> 2] |= (uint32_t)(quant_code(__fmul_rn(s, f[j]), sn, 127) & 0xFF) << ((j & 3) * 8);
-  return make_uint4(o[0], o[1], o[2], o[3]);
+  return recode16_exact(v, s, sn, fa, fb);
 }
 
-__device__ __forceinline__ float amax16(uint4 v) {
-  float f[16];
-  floats16(v, f);
-  float m = 0.0f;
-#pragma unroll
-  for (int j = 0; j < 16; j += 2) m = fmaxf(m, fmaxf(fabsf(f[j]), fabsf(f[j + 1])));
-  return m;
-}
+// What a thread holds of a page of K or V: 16-byte chunks of gathered rows, per two of which
+// (evict) one scale, and a token's weight or position.
+template <int D, bool FILL>
+struct PageCfg {
+  static constexpr int kThreads = FILL ? 256 : 128;            // 32 bf16 values or 64 codes each
+  static constexpr int kChunks = FILL ? D / 8 : D / 16;        // of a row
+  static constexpr int kVec = kTile * kChunks / kThreads;
+  static constexpr int kRowThreads = FILL ? kChunks : 4;       // threads that share a row
+  static constexpr int kRowStep = kThreads / kRowThreads;      // rows a thread's chunks are apart
+  static constexpr int kRowsEach = kTile / kRowStep;           // rows per thread
+  static constexpr int kPerRow = kVec / kRowsEach;             // chunks of each
+};
 
 template <int D, bool FILL>
-__global__ void __launch_bounds__(256) paged_write_kernel(const PagedCutParams p) {
-  __shared__ float red[16];
-  const int i = blockIdx.x, g = blockIdx.y, b = blockIdx.z, t = threadIdx.x;
+struct PageRows {
+  using C = PageCfg<D, FILL>;
+  uint4 v[C::kVec];
+  float s[FILL ? 1 : C::kRowsEach];
+  uint32_t side;  // weight bits or position of token t of the page (t < 64)
+  int page;       // destination
+};
+
+// The K (V) part of pages i0 .. i0 + per - 1 of one row.  While a page's values are reduced and
+// written the next page's rows are on their way.
+template <int D, bool FILL>
+__global__ void __launch_bounds__(PageCfg<D, FILL>::kThreads, FILL ? 4 : 7)
+    paged_write_kernel(const PagedCutParams p, int per, int groups) {
+  using C = PageCfg<D, FILL>;
+  constexpr int NT = C::kThreads;
+  __shared__ float red[2][NT / 32];
+  const int is_v = blockIdx.x & 1, grp_i = blockIdx.x >> 1, g = blockIdx.y, b = blockIdx.z, t = threadIdx.x;
   const tra_paged_cache& c = p.c;
-  const int4 st = p.ws_state[b];
-  if (i == 0 && g == 0 && t == 0) {
-    int4* const so = reinterpret_cast<int4*>(p.state_out) + b;
-    int4 s = FILL ? make_int4(st.x, st.y, st.z, 0) : reinterpret_cast<const int4*>(c.state)[b];
-    if (!FILL && st.w) s.x = st.x;
-    *so = s;
-  }
-  if (!st.w) return;
+  const int4 st = p.ws_state[b];  // fill {pages, tail, seen, 1}, evict {pages before, tail, valid, cut}
   const int row = b * c.Hkv + g;
-  if (FILL && i == p.keep) {  // the tail's rows
-    const int from = __ldg(p.cu + b) + st.z - st.y;
-    for (int f = t; f < st.y * (D / 8); f += 256) {
-      const int r = f / (D / 8), ch = f % (D / 8) * 8;
-      const long long src = ((long long)(from + r) * c.Hkv + g) * D + ch;
-      const long long dst = ((long long)row * kTile + r) * D + ch;
-      *reinterpret_cast<uint4*>(c.k_tail + dst) = *reinterpret_cast<const uint4*>(p.k + src);
-      *reinterpret_cast<uint4*>(c.v_tail + dst) = *reinterpret_cast<const uint4*>(p.v + src);
+  const long long row64 = (long long)row * (c.cap + 1) * kTile;
+  const int32_t* const table = c.table + (long long)row * c.cap;
+  float* const w_out = p.weight_out + row64;
+  int32_t* const p_out = p.pos_out + row64;
+
+  if (grp_i == groups) {  // what lies behind the pages
+    const int4 old = reinterpret_cast<const int4*>(c.state)[b];
+    if (FILL) {  // the tail's rows, weights and positions
+      const int from = __ldg(p.cu + b) + st.z - st.y;
+      const uint16_t* const x = is_v ? p.v : p.k;
+      uint16_t* const tail = is_v ? c.v_tail : c.k_tail;
+      for (int f = t; f < st.y * (D / 8); f += NT) {
+        const int r = f / (D / 8), ch = f % (D / 8) * 8;
+        *reinterpret_cast<uint4*>(tail + ((long long)row * kTile + r) * D + ch) =
+            *reinterpret_cast<const uint4*>(x + ((long long)(from + r) * c.Hkv + g) * D + ch);
+      }
+      if (t < st.y) {
+        if (is_v) p_out[st.x * kTile + t] = st.z - st.y + t;
+        else w_out[st.x * kTile + t] = p.imp ? p.imp[(long long)(from + t) * c.Hkv + g] : 0.0f;
+      }
+      if (g == 0 && !is_v && t == 0) reinterpret_cast<int4*>(p.state_out)[b] = make_int4(st.x, st.y, st.z, 0);
+      return;
     }
+    // evict: tail weights and positions; a row that stays moves over whole, where that is elsewhere
+    const int n = st.x, keep = p.keep, m0 = st.w ? n * kTile : 0, d0 = st.w ? keep * kTile : 0;
+    const int cnt = st.w ? st.y : (st.z && !p.in_place) ? n * kTile + st.y : 0;
+    for (int k = t; k < cnt; k += NT) {
+      if (is_v) p_out[d0 + k] = c.pos[row64 + m0 + k];
+      else w_out[d0 + k] = c.weight[row64 + m0 + k];
+    }
+    if (is_v && !p.in_place)  // the table turns by the new pages
+      for (int k = t; k < c.cap; k += NT)
+        p.table_out[(long long)row * c.cap + k] =
+            table[!st.w || k >= n + keep ? k : k < keep ? n + k : k - keep];
+    if (g == 0 && !is_v && t == 0)
+      reinterpret_cast<int4*>(p.state_out)[b] = make_int4(st.w ? keep : old.x, old.y, old.z, old.w);
     return;
   }
-  if (i >= st.x) return;
-  const int page = p.ws_dst[(long long)row * c.cap + i];
-  if (page < 0) return;
-  const int32_t* const src = p.ws_src + ((long long)row * c.cap + i) * kTile;
-  if constexpr (FILL) {
-    const long long from = __ldg(p.cu + b);
-    auto at = [&](const uint16_t* x, int r) { return x + ((from + src[r]) * c.Hkv + g) * D; };
-    quantise_page<D>(c, page, [&](int r) { return at(p.k, r); }, [&](int r) { return at(p.v, r); }, red);
-  } else {
-    constexpr int kChunks = D / 16, kPasses = kTile * kChunks / 256;
-    uint4 kx[kPasses], vx[kPasses];
-    float ks[kPasses], vs[kPasses];
+  const int i0 = grp_i * per, i1 = min(i0 + per, !st.w ? 0 : FILL ? st.x : p.keep);
+  if (i0 >= i1) return;
+  int8_t* const codes = is_v ? c.v8 : c.k8;
+  float* const scales = is_v ? c.sv : c.sk;
+  const long long from = FILL ? __ldg(p.cu + b) : 0;
+  const int r0 = t / C::kRowThreads, ch0 = t % C::kRowThreads;
+
+  // the thread's survivors of page i: their rows' sources and, for t < 64, token t
+  auto sources = [&](int i, int (&src)[C::kRowsEach], int& tok) {
+    const int32_t* const s = p.ws_src + ((long long)row * c.cap + i) * kTile;
+    const int32_t* const r = FILL ? s : p.ws_row + ((long long)row * c.cap + i) * kTile;
 #pragma unroll
-    for (int y = 0; y < kPasses; ++y) {
-      const int f = y * 256 + t;
-      const int from = src[f / kChunks];
-      const long long at = (long long)from * D + (f % kChunks) * 16;
-      kx[y] = *reinterpret_cast<const uint4*>(c.k8 + at);
-      vx[y] = *reinterpret_cast<const uint4*>(c.v8 + at);
-      ks[y] = c.sk[from / kTile];
-      vs[y] = c.sv[from / kTile];
-    }
-    // fl32(s * code) grows with |code|: the largest of a chunk is s times its largest code
-    float ka = 0.0f, va = 0.0f;
+    for (int y = 0; y < C::kRowsEach; ++y) src[y] = r[r0 + y * C::kRowStep];
+    tok = t < kTile ? s[t] : 0;
+  };
+  auto fetch = [&](int i, const int (&src)[C::kRowsEach], int tok, PageRows<D, FILL>& x) {
 #pragma unroll
-    for (int y = 0; y < kPasses; ++y) {
-      ka = fmaxf(ka, __fmul_rn(ks[y], amax16(kx[y])));
-      va = fmaxf(va, __fmul_rn(vs[y], amax16(vx[y])));
-    }
-    const float2 am = block_max2(ka, va, red);
-    const float sk = __fdiv_rn(am.x, 127.0f), sv = __fdiv_rn(am.y, 127.0f);
-    if (t == 0) {
-      c.sk[page] = sk;
-      c.sv[page] = sv;
-    }
-    int8_t* const k8 = c.k8 + (long long)page * kTile * D;
-    int8_t* const v8 = c.v8 + (long long)page * kTile * D;
+    for (int y = 0; y < C::kRowsEach; ++y) {
+      if constexpr (FILL) {
+        const uint16_t* const a = (is_v ? p.v : p.k) + ((from + src[y]) * c.Hkv + g) * D;
 #pragma unroll
-    for (int y = 0; y < kPasses; ++y) {
-      const int f = y * 256 + t;
-      *reinterpret_cast<uint4*>(k8 + f * 16) = recode16(kx[y], ks[y], sk, sk > 0.0f ? __fdiv_rn(ks[y], sk) : 0.0f);
-      *reinterpret_cast<uint4*>(v8 + f * 16) = recode16(vx[y], vs[y], sv, sv > 0.0f ? __fdiv_rn(vs[y], sv) : 0.0f);
+        for (int k = 0; k < C::kPerRow; ++k)
+          x.v[y * C::kPerRow + k] = *reinterpret_cast<const uint4*>(a + (ch0 + k * C::kRowThreads) * 8);
+      } else {
+        const int8_t* const a = codes + (long long)src[y] * D;
+#pragma unroll
+        for (int k = 0; k < C::kPerRow; ++k)
+          x.v[y * C::kPerRow + k] = *reinterpret_cast<const uint4*>(a + (ch0 + k * C::kRowThreads) * 16);
+        x.s[y] = scales[src[y] / kTile];
+      }
     }
+    if (t < kTile) {
+      if (is_v) x.side = FILL ? tok : c.pos[row64 + tok];
+      else x.side = __float_as_uint(FILL ? (p.imp ? p.imp[(from + tok) * c.Hkv + g] : 0.0f) : c.weight[row64 + tok]);
+    }
+    x.page = table[(FILL ? 0 : st.x) + i];
+  };
+  auto write = [&](int i, const PageRows<D, FILL>& x, float* r) {
+    if (t < kTile) {
+      if (is_v) p_out[i * kTile + t] = (int)x.side;
+      else w_out[i * kTile + t] = __uint_as_float(x.side);
+    }
+    float am = 0.0f;
+    if constexpr (FILL) {
+#pragma unroll
+      for (int k = 0; k < C::kVec; ++k) am = amax8(x.v[k], am);
+    } else {  // fl32(s * code) grows with |code|: a row's largest is s times its largest code
+#pragma unroll
+      for (int y = 0; y < C::kRowsEach; ++y) {
+        CodeRange range;
+        range.reset();
+#pragma unroll
+        for (int k = 0; k < C::kPerRow; ++k) range.add(x.v[y * C::kPerRow + k]);
+        am = fmaxf(am, __fmul_rn(x.s[y], range.largest()));
+      }
+    }
+    am = block_max<NT>(am, r);
+    if (x.page < 0 || x.page >= c.n_pool) {
+      if (t == 0) atomicOr(p.status, TRA_DEV_BAD_CACHE);
+      return;
+    }
+    int8_t* const dst = codes + (long long)x.page * kTile * D;
+    if constexpr (FILL) {
+      const BlockScale bs(am);
+      if (t == 0) scales[x.page] = bs.s;
+#pragma unroll
+      for (int y = 0; y < C::kRowsEach; ++y)
+#pragma unroll
+        for (int k = 0; k < C::kPerRow; ++k)
+          *reinterpret_cast<uint2*>(dst + (r0 + y * C::kRowStep) * D + (ch0 + k * C::kRowThreads) * 8) =
+              codes8(x.v[y * C::kPerRow + k], bs);
+    } else {
+      const float sn = __fdiv_rn(am, 127.0f), inv = recip(sn);
+      if (t == 0) scales[x.page] = sn;
+#pragma unroll
+      for (int y = 0; y < C::kRowsEach; ++y) {
+        const float f = x.s[y] * inv;
+        const float fa = f * kAbove, fb = f * kBelow;
+#pragma unroll
+        for (int k = 0; k < C::kPerRow; ++k)
+          *reinterpret_cast<uint4*>(dst + (r0 + y * C::kRowStep) * D + (ch0 + k * C::kRowThreads) * 16) =
+              recode16(x.v[y * C::kPerRow + k], x.s[y], sn, fa, fb);
+      }
+    }
+  };
+
+  int src[C::kRowsEach], tok;
+  PageRows<D, FILL> x0, x1;
+  sources(i0, src, tok);
+  fetch(i0, src, tok, x0);
+  if (i0 + 1 < i1) sources(i0 + 1, src, tok);
+  for (int i = i0; i < i1; i += 2) {
+    if (i + 1 < i1) fetch(i + 1, src, tok, x1);
+    if (i + 2 < i1) sources(i + 2, src, tok);
+    write(i, x0, red[0]);
+    if (i + 1 >= i1) break;
+    if (i + 2 < i1) fetch(i + 2, src, tok, x0);
+    if (i + 3 < i1) sources(i + 3, src, tok);
+    write(i + 1, x1, red[1]);
   }
+}
+
+// In place: the weights and positions of a row that was cut come back from the workspace,
+// and its table turns (the old pages move up by `keep`, the last ones first).
+__global__ void __launch_bounds__(kSelThreads) paged_settle_kernel(const PagedCutParams p) {
+  const int g = blockIdx.x, b = blockIdx.y, t = threadIdx.x;
+  const tra_paged_cache& c = p.c;
+  const int4 st = p.ws_state[b];
+  if (!st.w) return;
+  const int row = b * c.Hkv + g, keep = p.keep, n = st.x;
+  const long long row64 = (long long)row * (c.cap + 1) * kTile;
+  for (int k = t; k < keep * kTile + st.y; k += kSelThreads) {
+    c.weight[row64 + k] = p.weight_out[row64 + k];
+    c.pos[row64 + k] = p.pos_out[row64 + k];
+  }
+  int32_t* const table = c.table + (long long)row * c.cap;
+  int32_t* const fresh = p.ws_dst + (long long)row * c.cap;
+  for (int k = t; k < keep; k += kSelThreads) fresh[k] = table[n + k];
+  __syncthreads();
+  for (int hi = n; hi > 0; hi -= kSelThreads) {
+    const int k = hi - 1 - t;
+    const int page = k >= 0 ? table[k] : 0;
+    __syncthreads();
+    if (k >= 0) table[keep + k] = page;
+    __syncthreads();
+  }
+  for (int k = t; k < keep; k += kSelThreads) table[k] = fresh[k];
 }
 
 template <bool FILL>
 cudaError_t launch_cut(const PagedCutParams& p, cudaStream_t s) {
   const tra_paged_cache& c = p.c;
-  const int stage = p.nmax < kStageMax ? p.nmax : kStageMax;
+  const int stage = p.nmax < kSpan ? p.nmax : kSpan;
   const size_t smem = ((size_t)stage * 4 + 15) & ~(size_t)15;
-  cudaError_t e = cudaFuncSetAttribute(paged_select_kernel<FILL>, cudaFuncAttributeMaxDynamicSharedMemorySize, kStageMax * 4);
+  cudaError_t e = cudaFuncSetAttribute(paged_select_kernel<FILL>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSpan * 4);
   if (e != cudaSuccess) return e;
   paged_select_kernel<FILL><<<dim3(c.Hkv, c.B), kSelThreads, smem, s>>>(p, stage);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  const dim3 grid(p.keep + (FILL ? 1 : 0), c.Hkv, c.B);
+  // one page per CTA until every SM has its fill of them, then up to four
+  const long long ctas = 2ll * p.keep * c.Hkv * c.B;
+  const int per = ctas >= 4 * 148 * 8 ? 4 : ctas >= 2 * 148 * 8 ? 2 : 1;
+  const int groups = (p.keep + per - 1) / per;
+  const dim3 grid(2 * (groups + 1), c.Hkv, c.B);
   if (c.d == 128)
-    paged_write_kernel<128, FILL><<<grid, 256, 0, s>>>(p);
+    paged_write_kernel<128, FILL><<<grid, PageCfg<128, FILL>::kThreads, 0, s>>>(p, per, groups);
   else
-    paged_write_kernel<64, FILL><<<grid, 256, 0, s>>>(p);
+    paged_write_kernel<64, FILL><<<grid, PageCfg<64, FILL>::kThreads, 0, s>>>(p, per, groups);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || !p.in_place) return e;
+  paged_settle_kernel<<<dim3(c.Hkv, c.B), kSelThreads, 0, s>>>(p);
   return cudaGetLastError();
 }
 

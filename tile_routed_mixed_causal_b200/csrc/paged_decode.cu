@@ -35,7 +35,7 @@ namespace {
 constexpr int kCons = 4;                       // consumer warps
 constexpr int kStepThreads = 32 * (kCons + 1);
 constexpr int kPieces = 296;                   // CTAs of the list: two per SM
-constexpr int kFinThreads = 256;
+constexpr int kFinThreads = 128;
 constexpr float kSlack = 8.0f;                 // log2 units p may pass 1 before a rescale
 
 __device__ __forceinline__ float ex2(float x) {
@@ -66,6 +66,14 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t a) {
   uint32_t d;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
   return d;
+}
+// TMA copy of a page, which nobody reads again in this step: first to leave the L2 cache, so
+// that the scores stay there for the finish
+__device__ __forceinline__ void tma_load_page(uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t y, uint64_t pol) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%3, %4}], [%2], %5;" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(0), "r"(y), "l"(pol)
+      : "memory");
 }
 // two bytes of x (biased by 128) as exact f16
 __device__ __forceinline__ uint32_t h2_of(uint32_t x, uint32_t sel) {
@@ -102,7 +110,7 @@ struct ListPos {
   int b, g, item;
 };
 __device__ __forceinline__ long long list_scan(const int4* state, int B, int Hkv, int cap, long long at, bool find,
-                                               ListPos& pos, long long* before_b = nullptr, int want_b = -1) {
+                                               ListPos& pos) {
   const int lane = threadIdx.x & 31;
   long long base = 0;
   for (int b0 = 0; b0 < B; b0 += 32) {
@@ -127,7 +135,6 @@ __device__ __forceinline__ long long list_scan(const int4* state, int B, int Hkv
         pos.item = (int)((at - l0) % n);
       }
     }
-    if (before_b && want_b >= b0 && want_b < b0 + 32) *before_b = __shfl_sync(0xffffffffu, lo, want_b - b0);
     base += __shfl_sync(0xffffffffu, s, 31);
   }
   return base;
@@ -211,6 +218,8 @@ __global__ void __launch_bounds__(kStepThreads, 2)
     // ---------------------------------------------------------------- producer
     int issued = 0;
     bool bad = false;
+    uint64_t pol;
+    asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(pol));
     for_rows([&](int b, int g, int4 st, int i0, int i1) -> bool {
       const int32_t* const tab = c.table + ((long long)b * c.Hkv + g) * c.cap;
       const int end = min(i1, st.x);
@@ -240,8 +249,8 @@ __global__ void __launch_bounds__(kStepThreads, 2)
             scale[s] = make_float2(sx, sy);
             const uint32_t dst = base + s * C::kStageBytes;
             mbar_arrive_expect_tx(bar_full + s * 8, C::kStageBytes);
-            tma_load_2d(dst, &m.k8, bar_full + s * 8, 0, pk * kTile);
-            tma_load_2d(dst + C::kTileBytes, &m.v8, bar_full + s * 8, 0, pk * kTile);
+            tma_load_page(dst, &m.k8, bar_full + s * 8, pk * kTile, pol);
+            tma_load_page(dst + C::kTileBytes, &m.v8, bar_full + s * 8, pk * kTile, pol);
           }
         }
       }
@@ -507,6 +516,8 @@ __global__ void __launch_bounds__(kStepThreads, 2)
       }
       cons_sync();
       const long long slot = (long long)blockIdx.x + row;  // (piece, row) pairs rise along the list
+      if (t == 0 && i0 == 0) p.row_info[row].x = blockIdx.x;
+      if (t == 0 && i1 == st.x + 1) p.row_info[row].y = blockIdx.x;
       for (int x = t; x < grp * (D / 2); x += 32 * kCons) {
         const int gg = x / (D / 2), ch = x % (D / 2) * 2;
         float M = -INFINITY;
@@ -535,19 +546,19 @@ __global__ void __launch_bounds__(kStepThreads, 2)
 }
 
 // One CTA per (chunk of tokens, KV head, sequence).
-template <int D>
-__global__ void __launch_bounds__(kFinThreads) paged_finish_kernel(const PagedStepParams p, int chunk) {
-  __shared__ float s_m[8], s_il[8];
-  __shared__ float s_red[16];
-  __shared__ int s_first, s_cnt;
+template <int D, int GS>
+__global__ void __launch_bounds__(kFinThreads, 8) paged_finish_kernel(const PagedStepParams p, int chunk) {
+  __shared__ float s_w[GS * kPieces];  // pieces' m, then their weights 2^(m - M) / L
+  __shared__ float s_m[GS], s_il[GS];
+  __shared__ float s_red[kFinThreads / 32 * D];
   const tra_paged_cache& c = p.c;
   const int x = blockIdx.x, g = blockIdx.y, b = blockIdx.z, t = threadIdx.x, warp = t >> 5, lane = t & 31;
-  const int4 st = p.ws_state[b];
   const int row = b * c.Hkv + g, grp = c.Hq / c.Hkv;
+  const int4 st = p.ws_state[b];
+  const int2 info = p.row_info[row];
   const long long row64 = (long long)row * (c.cap + 1) * kTile;
-  const int n_items = row_items(st, c.cap);
   const int tok = st.x * kTile + st.y;  // tokens before the step
-  if (n_items == 0) {  // idle, bad or full: the row stays
+  if (row_items(st, c.cap) == 0) {  // idle, bad or full: the row stays
     const PagedRow kind = paged_row(st, c.cap);
     if (x == 0 && g == 0 && t == 0) {
       reinterpret_cast<int4*>(p.state_out)[b] = st;
@@ -561,70 +572,92 @@ __global__ void __launch_bounds__(kFinThreads) paged_finish_kernel(const PagedSt
   const int total = tok + 1;
   if ((long long)x * chunk >= total) return;
   const int chunks = (total + chunk - 1) / chunk;
-
-  // the pieces that hold items of this row
-  if (warp == 0) {
-    ListPos pos{0, 0, 0};
-    long long before = 0;
-    const long long items = list_scan(p.ws_state, c.B, c.Hkv, c.cap, 0, false, pos, &before, b);
-    const int pieces = pieces_of(items);
-    const long long r0 = before + (long long)g * n_items, r1 = r0 + n_items - 1;
-    auto piece_at = [&](long long item) {
-      int i = (int)(item * pieces / items);
-      while (piece_start(items, pieces, i + 1) <= item) ++i;
-      while (piece_start(items, pieces, i) > item) --i;
-      return i;
-    };
-    if (lane == 0) {
-      s_first = piece_at(r0);
-      s_cnt = piece_at(r1) - s_first + 1;
+  const long long slot0 = (long long)info.x + row;
+  const int cnt = info.y - info.x + 1;
+  for (int h = warp; h < grp; h += kFinThreads / 32) {
+    float M = -INFINITY, L = 0.0f;
+    for (int i = lane; i < cnt; i += 32) {  // running maximum and sum over this lane's pieces
+      const float2 v = *reinterpret_cast<const float2*>(p.part_ml + ((slot0 + i) * grp + h) * 2);
+      s_w[h * kPieces + i] = v.x;
+      if (v.x > M) {
+        L *= ex2(M - v.x);
+        M = v.x;
+      }
+      if (v.x != -INFINITY) L += v.y * ex2(v.x - M);
     }
-  }
-  __syncthreads();
-  const long long slot0 = (long long)s_first + row;
-  const int cnt = s_cnt;
-  if (warp < grp) {
-    float M = -INFINITY;
-    for (int i = lane; i < cnt; i += 32) M = fmaxf(M, p.part_ml[((slot0 + i) * grp + warp) * 2]);
+    float MM = M;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    float L = 0.0f;
-    for (int i = lane; i < cnt; i += 32) {
-      const float2 v = *reinterpret_cast<const float2*>(p.part_ml + ((slot0 + i) * grp + warp) * 2);
-      L += v.x == -INFINITY ? 0.0f : v.y * ex2(v.x - M);
-    }
+    for (int o = 16; o > 0; o >>= 1) MM = fmaxf(MM, __shfl_xor_sync(0xffffffffu, MM, o));
+    L = M == -INFINITY ? 0.0f : L * ex2(M - MM);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+    const float il = 1.0f / L;
     if (lane == 0) {
-      s_m[warp] = M;
-      s_il[warp] = 1.0f / L;
+      s_m[h] = MM;
+      s_il[h] = il;
+    }
+    for (int i = lane; i < cnt; i += 32) {
+      const float m = s_w[h * kPieces + i];
+      s_w[h * kPieces + i] = m == -INFINITY ? 0.0f : ex2(m - MM) * il;
     }
   }
   __syncthreads();
 
-  // outputs: head x, x + chunks, ...
+  // outputs of heads x, x + chunks, ...: a warp takes every fourth piece, then they are joined
   for (int gg = x; gg < grp; gg += chunks) {
-    for (int ch = t; ch < D; ch += kFinThreads) {
-      float acc = 0.0f;
+    constexpr int kEach = D / 32;  // channels per lane
+    float acc[kEach];
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) acc[k] = 0.0f;
 #pragma unroll 4
-      for (int i = 0; i < cnt; ++i) {
-        const long long pi = (slot0 + i) * grp + gg;
-        const float mi = p.part_ml[pi * 2];
-        acc += mi == -INFINITY ? 0.0f : p.part_o[pi * D + ch] * ex2(mi - s_m[gg]);
-      }
-      const __nv_bfloat16 r = __float2bfloat16_rn(acc * s_il[gg]);
+    for (int i = warp; i < cnt; i += kFinThreads / 32) {
+      const float w = s_w[gg * kPieces + i];
+      const float* const o = p.part_o + ((slot0 + i) * grp + gg) * D + lane * kEach;
+      float v[kEach];
+      if constexpr (kEach == 4) *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(o);
+      else *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(o);
+#pragma unroll
+      for (int k = 0; k < kEach; ++k) acc[k] += v[k] * w;
+    }
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) s_red[warp * D + lane * kEach + k] = acc[k];
+    __syncthreads();
+    for (int ch = t; ch < D; ch += kFinThreads) {
+      float o = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kFinThreads / 32; ++w) o += s_red[w * D + ch];
+      const __nv_bfloat16 r = __float2bfloat16_rn(o);
       p.out[((long long)b * c.Hq + g * grp + gg) * D + ch] = *reinterpret_cast<const uint16_t*>(&r);
     }
+    __syncthreads();
   }
   // weights: a token's probabilities over the group's heads, in order
-  const int gs = paged_score_stride(grp);
-  const float* const srow = p.scores + row64 * gs;
+  const float* const srow = p.scores + row64 * GS;
   const int end = (int)min((long long)total, (long long)(x + 1) * chunk);
+  float hm[GS], hl[GS];  // (a padded head adds nothing)
+#pragma unroll
+  for (int h = 0; h < GS; ++h) {
+    hm[h] = h < grp ? s_m[h] : 0.0f;
+    hl[h] = h < grp ? s_il[h] : 0.0f;
+  }
+#pragma unroll 4
   for (int i = x * chunk + t; i < end; i += kFinThreads) {
-    const float* const s = srow + (long long)i * gs;
+    const float* const src = srow + (long long)i * GS;
+    float s[GS];
+    if constexpr (GS % 4 == 0) {
+#pragma unroll
+      for (int h = 0; h < GS; h += 4) *reinterpret_cast<float4*>(s + h) = *reinterpret_cast<const float4*>(src + h);
+    } else if constexpr (GS % 2 == 0) {
+#pragma unroll
+      for (int h = 0; h < GS; h += 2) *reinterpret_cast<float2*>(s + h) = *reinterpret_cast<const float2*>(src + h);
+    } else {
+      s[0] = src[0];
+    }
+    const float old = i < tok ? c.weight[row64 + i] : 0.0f;
     float w = 0.0f;
-    for (int h = 0; h < grp; ++h) w += ex2(s[h] - s_m[h]) * s_il[h];
-    p.weight_out[row64 + i] = (i < tok ? c.weight[row64 + i] : 0.0f) + w;
+#pragma unroll
+    for (int h = 0; h < GS; ++h) w += ex2(s[h] - hm[h]) * hl[h];
+    p.weight_out[row64 + i] = old + w;
   }
   if (x != 0) return;
   if (st.y == kTile - 1) {  // the tail is full: the row's next page
@@ -634,7 +667,9 @@ __global__ void __launch_bounds__(kFinThreads) paged_finish_kernel(const PagedSt
     } else {
       const uint16_t* const kt = c.k_tail + (long long)row * kTile * D;
       const uint16_t* const vt = c.v_tail + (long long)row * kTile * D;
-      quantise_page<D>(c, page, [&](int r) { return kt + r * D; }, [&](int r) { return vt + r * D; }, s_red);
+      const long long at = (long long)page * kTile * D;
+      quantise_page<D, kFinThreads>([&](int r) { return kt + r * D; }, c.k8 + at, c.sk + page, s_red);
+      quantise_page<D, kFinThreads>([&](int r) { return vt + r * D; }, c.v8 + at, c.sv + page, s_red + kFinThreads / 32);
     }
   }
   if (g == 0 && t == 0)
@@ -657,13 +692,19 @@ cudaError_t launch_step_d(const PagedStepParams& p, const PagedMaps& m, cudaStre
   const int grp = c.Hq / c.Hkv;
   cudaError_t e = grp <= 2 ? launch_step_g<D, 2>(p, m, s) : grp <= 4 ? launch_step_g<D, 4>(p, m, s) : launch_step_g<D, 8>(p, m, s);
   if (e != cudaSuccess) return e;
-  // chunks of 256 tokens at least, and no more than about eight CTAs per SM over all rows
+  // chunks of 256 tokens at least, and about one wave of CTAs over all rows (eight per SM)
   const long long most = ((long long)c.cap + 1) * kTile, rows = (long long)c.B * c.Hkv;
-  long long per = (rows * most / 1184 + 255) / 256 * 256;
+  long long per = (rows * most / 1184 + 127) / 128 * 128;
   if (per < 256) per = 256;
   if (per > most) per = most;
   const dim3 grid((unsigned)((most + per - 1) / per), c.Hkv, c.B);
-  paged_finish_kernel<D><<<grid, kFinThreads, 0, s>>>(p, (int)per);
+  switch (paged_score_stride(grp)) {
+    case 1: paged_finish_kernel<D, 1><<<grid, kFinThreads, 0, s>>>(p, (int)per); break;
+    case 2: paged_finish_kernel<D, 2><<<grid, kFinThreads, 0, s>>>(p, (int)per); break;
+    case 4: paged_finish_kernel<D, 4><<<grid, kFinThreads, 0, s>>>(p, (int)per); break;
+    case 6: paged_finish_kernel<D, 6><<<grid, kFinThreads, 0, s>>>(p, (int)per); break;
+    default: paged_finish_kernel<D, 8><<<grid, kFinThreads, 0, s>>>(p, (int)per); break;
+  }
   return cudaGetLastError();
 }
 
@@ -676,13 +717,17 @@ PagedLayout paged_layout(const tra_paged_cache& c) {
   // the step's arrays and the cut's share the space behind the states
   l.state = 0;
   const size_t head = up((size_t)c.B * 16);
-  l.ml = head;
+  l.info = head;
+  l.ml = l.info + up(rows * 8);
   l.o = l.ml + up(slots * grp * 8);
   l.scores = l.o + up(slots * grp * c.d * 4);
   const size_t step_end = l.scores + up(rows * (c.cap + 1) * kTile * paged_score_stride((int)grp) * 4);
   l.src = head;
-  l.dst = l.src + up(rows * c.cap * kTile * 4);
-  const size_t cut_end = l.dst + up(rows * c.cap * 4);
+  l.row = l.src + up(rows * c.cap * kTile * 4);
+  l.dst = l.row + up(rows * c.cap * kTile * 4);
+  l.weight = l.dst + up(rows * c.cap * 4);
+  l.pos = l.weight + up(rows * (c.cap + 1) * kTile * 4);
+  const size_t cut_end = l.pos + up(rows * (c.cap + 1) * kTile * 4);
   l.total = step_end > cut_end ? step_end : cut_end;
   return l;
 }

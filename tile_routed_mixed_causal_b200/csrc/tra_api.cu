@@ -899,6 +899,7 @@ tra_status paged_cache_fill(const tra_paged_cache* cache, const tra_shape* shape
   p.status = status_dev;
   p.ws_state = reinterpret_cast<int4*>(ws + lay.state);
   p.ws_src = reinterpret_cast<int32_t*>(ws + lay.src);
+  p.ws_row = reinterpret_cast<int32_t*>(ws + lay.row);
   p.ws_dst = reinterpret_cast<int32_t*>(ws + lay.dst);
   cudaError_t e = tra::launch_paged_fill(p, reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "paged fill launch");
@@ -931,6 +932,7 @@ tra_status paged_attention_decode(const tra_paged_cache* cache, const uint16_t* 
   p.weight_out = weight_out ? weight_out : cache->weight;
   p.status = status_dev;
   p.ws_state = reinterpret_cast<int4*>(ws + lay.state);
+  p.row_info = reinterpret_cast<int2*>(ws + lay.info);
   p.part_ml = reinterpret_cast<float*>(ws + lay.ml);
   p.part_o = reinterpret_cast<float*>(ws + lay.o);
   p.scores = reinterpret_cast<float*>(ws + lay.scores);
@@ -952,8 +954,10 @@ tra_status paged_cache_evict(const tra_paged_cache* cache, int32_t keep, int32_t
   tra::PagedLayout lay;
   tra_status st = check_paged(cache, workspace, workspace_bytes, status_dev, &lay);
   if (st != TRA_OK) return st;
-  const int given = (state_out != nullptr) + (table_out != nullptr) + (weight_out != nullptr) + (pos_out != nullptr);
-  if (given != 0 && given != 4)
+  const int own = (state_out == nullptr || state_out == cache->state) + (table_out == nullptr || table_out == cache->table) +
+                  (weight_out == nullptr || weight_out == cache->weight) + (pos_out == nullptr || pos_out == cache->pos);
+  const bool given = own == 0;
+  if (own != 0 && own != 4)
     return fail(TRA_ERR_INVALID, "state_out, table_out, weight_out and pos_out are given together or not at all");
   if (!aligned16(state_out) || !aligned16(table_out) || !aligned16(weight_out) || !aligned16(pos_out))
     return fail(TRA_ERR_INVALID, "state_out/table_out/weight_out/pos_out must be 16-byte aligned");
@@ -967,11 +971,14 @@ tra_status paged_cache_evict(const tra_paged_cache* cache, int32_t keep, int32_t
   p.nmax = (int)std::min<int64_t>((int64_t)cache->cap * TRA_TILE, 1 << 30);
   p.state_out = given ? state_out : cache->state;
   p.table_out = given ? table_out : cache->table;
-  p.weight_out = given ? weight_out : cache->weight;
-  p.pos_out = given ? pos_out : cache->pos;
+  // in place: the moved weights and positions pass through the workspace
+  p.in_place = !given;
+  p.weight_out = given ? weight_out : reinterpret_cast<float*>(ws + lay.weight);
+  p.pos_out = given ? pos_out : reinterpret_cast<int32_t*>(ws + lay.pos);
   p.status = status_dev;
   p.ws_state = reinterpret_cast<int4*>(ws + lay.state);
   p.ws_src = reinterpret_cast<int32_t*>(ws + lay.src);
+  p.ws_row = reinterpret_cast<int32_t*>(ws + lay.row);
   p.ws_dst = reinterpret_cast<int32_t*>(ws + lay.dst);
   cudaError_t e = tra::launch_paged_evict(p, reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "paged evict launch");

@@ -211,6 +211,7 @@ struct PagedStepParams {
   float* weight_out;
   int32_t* status;
   int4* ws_state;        // [B]
+  int2* row_info;        // [B][Hkv] first and last CTA that had items of the row
   float* part_ml;        // [pieces][grp][2]
   float* part_o;         // [pieces][grp][d]
   float* scores;         // [B][Hkv][(cap + 1) * 64][paged_score_stride(grp)]
@@ -221,8 +222,8 @@ struct PagedMaps {
 };
 
 // Fill (src = prompt) and evict (src = the cache): select the survivors of every row, then
-// quantise them page by page.  Workspace: row states, the survivors' source rows and the
-// destination pages.
+// quantise them page by page.  Workspace: row states and the survivors' tokens; for an evict in
+// place also their weights and positions.
 struct PagedCutParams {
   tra_paged_cache c;
   int keep, recent;
@@ -238,13 +239,15 @@ struct PagedCutParams {
   float* weight_out;
   int32_t* pos_out;
   int32_t* status;
-  int4* ws_state;        // [B] {pages after the call, tail, seen, 1 if the row is cut or filled}
-  int32_t* ws_src;       // [B][Hkv][keep * 64] token of the sequence, or page * 64 + slot
-  int32_t* ws_dst;       // [B][Hkv][keep] destination page, -1: none
+  int in_place;          // evict: weight_out and pos_out are the workspace's, settled afterwards
+  int4* ws_state;        // [B] what the selection found (paged_write_kernel)
+  int32_t* ws_src;       // [B][Hkv][cap * 64] the survivors' tokens, ascending
+  int32_t* ws_row;       // evict: [B][Hkv][cap * 64] their rows in the codes (page * 64 + slot)
+  int32_t* ws_dst;       // [B][Hkv][cap] scratch of the settling
 };
 
 struct PagedLayout {     // byte offsets in the workspace
-  size_t state, ml, o, scores, src, dst, total;
+  size_t state, ml, o, scores, info, src, row, dst, weight, pos, total;
 };
 PagedLayout paged_layout(const tra_paged_cache& c);
 // floats per token in the score array: the group's heads, an even number above one
