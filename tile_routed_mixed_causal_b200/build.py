@@ -18,7 +18,7 @@ OUT = os.path.join(PKG, "libtra.so")
 BUILD = os.path.join(PKG, "_build")
 SOURCES = ["tra_api.cu", "quantize.cu", "lists.cu", "prefill.cu", "decode.cu",
            "decode_noalloc.cu", "selftest.cu", "hybrid.cu", "weights.cu", "paged_cut.cu", "paged_decode.cu"]
-HEADERS = ["tra_device.cuh", "tra_launch.h", "paged_device.cuh"]
+HEADERS = ["tra_device.cuh", "tra_launch.h", "paged_device.cuh", "launch_ex.cuh"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 

@@ -17,6 +17,7 @@
 // third kernel, since pages are written in any order.
 #include <cuda_fp16.h>
 
+#include "launch_ex.cuh"
 #include "paged_device.cuh"
 
 namespace tra {
@@ -68,6 +69,7 @@ __global__ void __launch_bounds__(kSelThreads) paged_select_kernel(const PagedCu
   __shared__ uint32_t tmp[33];
   __shared__ uint2 warp_sum[kSpanChunks * 32 + 1];
   __shared__ uint32_t s_bin, s_want;
+  grid_release();
   const int g = blockIdx.x, b = blockIdx.y, t = threadIdx.x, warp = t >> 5, lane = t & 31;
   const tra_paged_cache& c = p.c;
   const int row = b * c.Hkv + g;
@@ -379,6 +381,8 @@ __global__ void __launch_bounds__(PageCfg<D, FILL>::kThreads, FILL ? 4 : 7)
   __shared__ float red[2][NT / 32];
   const int is_v = blockIdx.x & 1, grp_i = blockIdx.x >> 1, g = blockIdx.y, b = blockIdx.z, t = threadIdx.x;
   const tra_paged_cache& c = p.c;
+  grid_release();
+  grid_wait();
   const int4 st = p.ws_state[b];  // fill {pages, tail, seen, 1}, evict {pages before, tail, valid, cut}
   const int row = b * c.Hkv + g;
   const long long row64 = (long long)row * (c.cap + 1) * kTile;
@@ -526,6 +530,7 @@ __global__ void __launch_bounds__(PageCfg<D, FILL>::kThreads, FILL ? 4 : 7)
 __global__ void __launch_bounds__(kSelThreads) paged_settle_kernel(const PagedCutParams p) {
   const int g = blockIdx.x, b = blockIdx.y, t = threadIdx.x;
   const tra_paged_cache& c = p.c;
+  grid_wait();
   const int4 st = p.ws_state[b];
   if (!st.w) return;
   const int row = b * c.Hkv + g, keep = p.keep, n = st.x;
@@ -553,24 +558,20 @@ cudaError_t launch_cut(const PagedCutParams& p, cudaStream_t s) {
   const tra_paged_cache& c = p.c;
   const int stage = p.nmax < kSpan ? p.nmax : kSpan;
   const size_t smem = ((size_t)stage * 4 + 15) & ~(size_t)15;
-  cudaError_t e = cudaFuncSetAttribute(paged_select_kernel<FILL>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSpan * 4);
+  static SmemLimit limit;
+  cudaError_t e = limit.raise(paged_select_kernel<FILL>, kSpan * 4);
   if (e != cudaSuccess) return e;
-  paged_select_kernel<FILL><<<dim3(c.Hkv, c.B), kSelThreads, smem, s>>>(p, stage);
-  e = cudaGetLastError();
+  e = launch_ex(paged_select_kernel<FILL>, dim3(c.Hkv, c.B), kSelThreads, smem, s, 0, false, p, stage);
   if (e != cudaSuccess) return e;
   // one page per CTA until every SM has its fill of them, then up to four
   const long long ctas = 2ll * p.keep * c.Hkv * c.B;
   const int per = ctas >= 4 * 148 * 8 ? 4 : ctas >= 2 * 148 * 8 ? 2 : 1;
   const int groups = (p.keep + per - 1) / per;
   const dim3 grid(2 * (groups + 1), c.Hkv, c.B);
-  if (c.d == 128)
-    paged_write_kernel<128, FILL><<<grid, PageCfg<128, FILL>::kThreads, 0, s>>>(p, per, groups);
-  else
-    paged_write_kernel<64, FILL><<<grid, PageCfg<64, FILL>::kThreads, 0, s>>>(p, per, groups);
-  e = cudaGetLastError();
+  e = c.d == 128 ? launch_ex(paged_write_kernel<128, FILL>, grid, PageCfg<128, FILL>::kThreads, 0, s, 0, true, p, per, groups)
+                 : launch_ex(paged_write_kernel<64, FILL>, grid, PageCfg<64, FILL>::kThreads, 0, s, 0, true, p, per, groups);
   if (e != cudaSuccess || !p.in_place) return e;
-  paged_settle_kernel<<<dim3(c.Hkv, c.B), kSelThreads, 0, s>>>(p);
-  return cudaGetLastError();
+  return launch_ex(paged_settle_kernel, dim3(c.Hkv, c.B), kSelThreads, 0, s, 0, true, p);
 }
 
 }  // namespace

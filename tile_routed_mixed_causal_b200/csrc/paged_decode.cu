@@ -27,6 +27,7 @@
 // bounds the step: 2 d bytes of codes per cached token, against 4 grp + 8 bytes here.
 #include <cuda_fp16.h>
 
+#include "launch_ex.cuh"
 #include "paged_device.cuh"
 
 namespace tra {
@@ -177,6 +178,7 @@ __global__ void __launch_bounds__(kStepThreads, 2)
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
   const int grp = c.Hq / c.Hkv;
 
+  grid_release();
   if (t == 0) {
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(bar_full + s * 8, 1);
@@ -554,6 +556,7 @@ __global__ void __launch_bounds__(kFinThreads, 8) paged_finish_kernel(const Page
   const tra_paged_cache& c = p.c;
   const int x = blockIdx.x, g = blockIdx.y, b = blockIdx.z, t = threadIdx.x, warp = t >> 5, lane = t & 31;
   const int row = b * c.Hkv + g, grp = c.Hq / c.Hkv;
+  grid_wait();
   const int4 st = p.ws_state[b];
   const int2 info = p.row_info[row];
   const long long row64 = (long long)row * (c.cap + 1) * kTile;
@@ -640,24 +643,35 @@ __global__ void __launch_bounds__(kFinThreads, 8) paged_finish_kernel(const Page
     hm[h] = h < grp ? s_m[h] : 0.0f;
     hl[h] = h < grp ? s_il[h] : 0.0f;
   }
-#pragma unroll 4
-  for (int i = x * chunk + t; i < end; i += kFinThreads) {
-    const float* const src = srow + (long long)i * GS;
-    float s[GS];
-    if constexpr (GS % 4 == 0) {
+  // (a batch of loads before its stores: the compiler cannot tell their arrays apart)
+  constexpr int kBatch = GS > 4 ? 2 : 4;
+  for (int i0 = x * chunk + t; i0 < end; i0 += kBatch * kFinThreads) {
+    float s[kBatch][GS], old[kBatch];
 #pragma unroll
-      for (int h = 0; h < GS; h += 4) *reinterpret_cast<float4*>(s + h) = *reinterpret_cast<const float4*>(src + h);
-    } else if constexpr (GS % 2 == 0) {
+    for (int k = 0; k < kBatch; ++k) {
+      const int i = i0 + k * kFinThreads;
+      if (i >= end) break;
+      const float* const src = srow + (long long)i * GS;
+      if constexpr (GS % 4 == 0) {
 #pragma unroll
-      for (int h = 0; h < GS; h += 2) *reinterpret_cast<float2*>(s + h) = *reinterpret_cast<const float2*>(src + h);
-    } else {
-      s[0] = src[0];
+        for (int h = 0; h < GS; h += 4) *reinterpret_cast<float4*>(s[k] + h) = *reinterpret_cast<const float4*>(src + h);
+      } else if constexpr (GS % 2 == 0) {
+#pragma unroll
+        for (int h = 0; h < GS; h += 2) *reinterpret_cast<float2*>(s[k] + h) = *reinterpret_cast<const float2*>(src + h);
+      } else {
+        s[k][0] = src[0];
+      }
+      old[k] = i < tok ? c.weight[row64 + i] : 0.0f;
     }
-    const float old = i < tok ? c.weight[row64 + i] : 0.0f;
-    float w = 0.0f;
 #pragma unroll
-    for (int h = 0; h < GS; ++h) w += ex2(s[h] - hm[h]) * hl[h];
-    p.weight_out[row64 + i] = old + w;
+    for (int k = 0; k < kBatch; ++k) {
+      const int i = i0 + k * kFinThreads;
+      if (i >= end) break;
+      float w = 0.0f;
+#pragma unroll
+      for (int h = 0; h < GS; ++h) w += ex2(s[k][h] - hm[h]) * hl[h];
+      p.weight_out[row64 + i] = old[k] + w;
+    }
   }
   if (x != 0) return;
   if (st.y == kTile - 1) {  // the tail is full: the row's next page
@@ -680,10 +694,10 @@ __global__ void __launch_bounds__(kFinThreads, 8) paged_finish_kernel(const Page
 template <int D, int GRP>
 cudaError_t launch_step_g(const PagedStepParams& p, const PagedMaps& m, cudaStream_t s) {
   using C = StepCfg<D, GRP>;
-  cudaError_t e = cudaFuncSetAttribute(paged_step_kernel<D, GRP>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  static SmemLimit limit;
+  cudaError_t e = limit.raise(paged_step_kernel<D, GRP>, C::kSmem);
   if (e != cudaSuccess) return e;
-  paged_step_kernel<D, GRP><<<kPieces, kStepThreads, C::kSmem, s>>>(p, m);
-  return cudaGetLastError();
+  return launch_ex(paged_step_kernel<D, GRP>, dim3(kPieces), kStepThreads, C::kSmem, s, 0, false, p, m);
 }
 
 template <int D>
@@ -698,14 +712,14 @@ cudaError_t launch_step_d(const PagedStepParams& p, const PagedMaps& m, cudaStre
   if (per < 256) per = 256;
   if (per > most) per = most;
   const dim3 grid((unsigned)((most + per - 1) / per), c.Hkv, c.B);
+  const int chunk = (int)per;
   switch (paged_score_stride(grp)) {
-    case 1: paged_finish_kernel<D, 1><<<grid, kFinThreads, 0, s>>>(p, (int)per); break;
-    case 2: paged_finish_kernel<D, 2><<<grid, kFinThreads, 0, s>>>(p, (int)per); break;
-    case 4: paged_finish_kernel<D, 4><<<grid, kFinThreads, 0, s>>>(p, (int)per); break;
-    case 6: paged_finish_kernel<D, 6><<<grid, kFinThreads, 0, s>>>(p, (int)per); break;
-    default: paged_finish_kernel<D, 8><<<grid, kFinThreads, 0, s>>>(p, (int)per); break;
+    case 1: return launch_ex(paged_finish_kernel<D, 1>, grid, kFinThreads, 0, s, 0, true, p, chunk);
+    case 2: return launch_ex(paged_finish_kernel<D, 2>, grid, kFinThreads, 0, s, 0, true, p, chunk);
+    case 4: return launch_ex(paged_finish_kernel<D, 4>, grid, kFinThreads, 0, s, 0, true, p, chunk);
+    case 6: return launch_ex(paged_finish_kernel<D, 6>, grid, kFinThreads, 0, s, 0, true, p, chunk);
+    default: return launch_ex(paged_finish_kernel<D, 8>, grid, kFinThreads, 0, s, 0, true, p, chunk);
   }
-  return cudaGetLastError();
 }
 
 }  // namespace

@@ -166,13 +166,13 @@ bool map_i8(CUtensorMap* m, const void* base, int row_bytes, int64_t rows, int b
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// bf16 [ntok][H][d] viewed as 3-D (d, H, ntok); boxes of 64 channels x 1 head x box_rows tokens.
-bool map_bf16(CUtensorMap* m, const void* base, int d, int H, int64_t ntok, int box_rows) {
+// bf16 [ntok][H][d] viewed as 3-D (d, H, ntok); boxes of 64 channels x box_heads heads x box_rows tokens.
+bool map_bf16(CUtensorMap* m, const void* base, int d, int H, int64_t ntok, int box_rows, int box_heads = 1) {
   auto fn = encode_fn();
   if (!fn) return false;
   cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)H, (cuuint64_t)ntok};
   cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)H * d * 2};
-  cuuint32_t box[3] = {64, 1, (cuuint32_t)box_rows};
+  cuuint32_t box[3] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_rows};
   cuuint32_t es[3] = {1, 1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, es,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
@@ -799,33 +799,41 @@ tra_status attention_weight_sums(const tra_shape* shape, const uint16_t* q, cons
   p.Hkv = shape->Hkv;
   p.d = shape->d;
   p.n_queries = n_queries;
-  // work units (128 rows) of both passes and their 128 x 128 tiles
+  // a short window shares its query tiles among as many heads of a group as fit
   const int64_t grp = shape->Hq / shape->Hkv;
+  int64_t w_max = 0;
+  for (int b = 0; b < shape->B; ++b) {
+    const int64_t T = shape->cu_seqlens_host[b + 1] - shape->cu_seqlens_host[b];
+    w_max = std::max(w_max, n_queries > 0 ? std::min<int64_t>(T, n_queries) : T);
+  }
+  while (grp % (2 << p.pack) == 0 && (128 >> (p.pack + 1)) >= w_max && p.pack < 7) ++p.pack;
+  // work units (128 rows) of both passes and their tiles
+  const int64_t qtok = 128 >> p.pack;
   int64_t q_tiles = 0, k_tiles = 0;  // most of a sequence
   for (int b = 0; b < shape->B; ++b) {
     const int64_t T = shape->cu_seqlens_host[b + 1] - shape->cu_seqlens_host[b];
     const int64_t W = n_queries > 0 ? std::min<int64_t>(T, n_queries) : T;
-    const int64_t nk = (T + 127) / 128, nq = (W + 127) / 128;
-    // key tiles that the queries see, of full tiles: nk for the last query tile, one less each
-    const int64_t tiles = nq * nk - nq * (nq - 1) / 2;
+    const int64_t nk = (T + 127) / 128, nq = (W + qtok - 1) / qtok;
+    // key tiles that the queries see: nk for the last query tile, one less each before it
+    const int64_t tiles = nq * nk - (p.pack ? 0 : nq * (nq - 1) / 2);
     q_tiles = std::max(q_tiles, nq);
     k_tiles = std::max(k_tiles, nk);
-    p.lse_steps += tiles * shape->Hq;
+    p.lse_steps += tiles * (shape->Hq >> p.pack);
     p.lse_longest = std::max<long long>(p.lse_longest, nk);
-    p.sum_steps += tiles * shape->Hq;
-    p.sum_longest = std::max<long long>(p.sum_longest, nq * grp);
+    p.sum_steps += tiles * (shape->Hq >> p.pack);
+    p.sum_longest = std::max<long long>(p.sum_longest, nq * (grp >> p.pack));
   }
-  p.lse_units = q_tiles * shape->B * shape->Hq;
+  p.lse_units = q_tiles * shape->B * (shape->Hq >> p.pack);
   p.sum_units = k_tiles * shape->B * shape->Hkv;
   p.ntok = ntok;
-  p.scale_log2 = softmax_scale * 1.4426950408889634f;
+  p.scale_log2 = (float)((double)softmax_scale * 1.4426950408889634074);
   p.lse_given = lse_given != 0;
   p.lse = lse;
   p.weights = weights;
   p.status = status_dev;
   tra::WeightMaps m;
   memset(&m, 0, sizeof m);
-  if (!map_bf16(&m.q, q, shape->d, shape->Hq, ntok, 128) || !map_bf16(&m.k, k, shape->d, shape->Hkv, ntok, 128))
+  if (!map_bf16(&m.q, q, shape->d, shape->Hq, ntok, 128 >> p.pack, 1 << p.pack) || !map_bf16(&m.k, k, shape->d, shape->Hkv, ntok, 128))
     return fail(TRA_ERR_CUDA, "cuTensorMapEncodeTiled failed (driver entry point or arguments)");
   cudaError_t e = tra::launch_weight_sums(p, m, reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "weight sums launch");
@@ -926,7 +934,7 @@ tra_status paged_attention_decode(const tra_paged_cache* cache, const uint16_t* 
   p.q = q;
   p.k_new = k_new;
   p.v_new = v_new;
-  p.scale_log2 = softmax_scale * 1.4426950408889634f;
+  p.scale_log2 = (float)((double)softmax_scale * 1.4426950408889634074);
   p.out = out;
   p.state_out = state_out ? state_out : cache->state;
   p.weight_out = weight_out ? weight_out : cache->weight;

@@ -186,13 +186,15 @@ struct WeightParams {
   float* lse;            // [Hq][ntok]
   float* weights;        // [ntok][Hkv]
   int32_t* status;
+  int pack;              // log2 of the heads that share a query tile
+  int stages;            // tile ring (set by the launch)
   // work units of the two passes (grid sizes), and their 128 x 128 tiles: all, of the longest
   long long lse_units, lse_steps, lse_longest;
   long long sum_units, sum_steps, sum_longest;
 };
 
 struct WeightMaps {
-  CUtensorMap q, k;      // bf16 (d, H, ntok), boxes of 64 channels x 128 tokens
+  CUtensorMap q, k;      // bf16 (d, H, ntok), boxes of 64 channels x 128 rows (q: 2^pack heads)
 };
 
 cudaError_t launch_weight_sums(const WeightParams& p, const WeightMaps& m, cudaStream_t s);

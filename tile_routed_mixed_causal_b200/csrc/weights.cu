@@ -10,6 +10,9 @@
 //          a thread owns a key and adds exp2(s c - lse2[column]), no exchange at all;
 //   lse:   rows = 128 queries of one head, columns = keys; a thread owns a query and keeps
 //          its running maximum and sum.
+// A tile of queries holds 128 >> pack tokens of 2^pack heads of a group, token-major: one head
+// in general, more where the window is short (64 queries: two heads, so the keys are read and
+// multiplied for both at once).
 // The scores live in TMEM and registers only.  Per element the kernel needs one product
 // column of the tensor cores (d multiply-adds, 4096 per SM and cycle) and one exponential
 // (16 per SM and cycle), so for d <= 128 the exponentials bound it.
@@ -21,6 +24,7 @@
 // Where there are few units a cluster of up to 8 CTAs shares one (every C-th tile each)
 // and joins the partial rows over distributed shared memory in rank order: the same call
 // gives the same bits.
+#include "launch_ex.cuh"
 #include "tra_device.cuh"
 #include "tra_launch.h"
 
@@ -38,20 +42,22 @@ constexpr float kLseSlack = 16.0f;
 template <int D>
 struct WCfg {
   static constexpr int kTileBytes = kRows * D * 2;
-  static constexpr int kStages = D == 128 ? 2 : 3;
+  // tile ring: as deep as two CTAs per SM allow, or (lone) one
+  static constexpr int kStages2 = D == 128 ? 2 : 4, kStages1 = D == 128 ? 5 : 8;
   static constexpr int kSlabs = D / 64;
   static constexpr int kOffA = 0;
-  static constexpr int kOffB = kTileBytes;
-  static constexpr int kOffCol = kOffB + kStages * kTileBytes;     // [kColSlots][128] float
+  static constexpr int kOffCol = kTileBytes;                        // [kColSlots][128] float
   static constexpr int kOffFlag = kOffCol + kColSlots * kRows * 4;  // [kColSlots][2] int
   static constexpr int kOffRed = kOffFlag + kColSlots * 2 * 4;      // [2][128] float2
   static constexpr int kOffBar = kOffRed + 2 * kRows * 8;
-  static constexpr int kNumBars = 1 + 2 * kStages + 4 + 2 * kColSlots + 1;
+  static constexpr int kNumBars = 1 + 2 * kStages1 + 4 + 2 * kColSlots + 1;
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;
-  static constexpr int kUsed = kOffMisc + 32 + 1024;
-  // at least 80 KB, so that no more than two CTAs share an SM: their S blocks fill its TMEM
-  static constexpr int kSmem = kUsed > 80 * 1024 ? kUsed : 80 * 1024;
-  static_assert(2 * (kSmem + 1024) <= 228 * 1024, "two CTAs per SM");
+  static constexpr int kOffB = (kOffMisc + 32 + 1023) / 1024 * 1024;  // the ring, last
+  static constexpr int smem(int stages) { return kOffB + stages * kTileBytes + 1024; }
+  // more than a third of an SM's shared memory each, so that no more than two CTAs share
+  // one: their S blocks fill its TMEM
+  static_assert(smem(kStages2) > 77 * 1024 && 2 * (smem(kStages2) + 1024) <= 228 * 1024, "two CTAs per SM");
+  static_assert(smem(kStages1) <= 227 * 1024, "one CTA per SM");
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -97,46 +103,46 @@ __device__ __forceinline__ void mma_bf16_e(uint32_t d_tmem, uint64_t a, uint64_t
 template <bool LSE>
 struct WUnit {
   bool valid;
-  int b, head;       // head: query head (lse), KV head (sums)
+  int b, head;       // head: first query head of the rows (lse), KV head (sums)
   int seq0, T, wq0;  // sequence start, length, first query of the window
-  int r0;            // first row (query or key) within the sequence
+  int r0;            // first row's position (query or key) within the sequence
   int ncol, c0;      // column tiles per head, the first of them
   int steps;         // tiles of the stream (all CTAs of the cluster)
 
   __device__ __forceinline__ void init(const WeightParams& p, long long id) {
-    const int H = LSE ? p.Hq : p.Hkv;
+    const int H = LSE ? p.Hq >> p.pack : p.Hkv;
     head = (int)(id % H);
     b = (int)((id / H) % p.B);
     const int t = (int)(id / ((long long)H * p.B));
     seq0 = __ldg(p.cu + b);
     T = __ldg(p.cu + b + 1) - seq0;
     const int W = p.n_queries > 0 ? min(T, p.n_queries) : T;
+    const int qtok = kRows >> p.pack;  // tokens of a query tile
+    const int nq = (W + qtok - 1) / qtok;
     wq0 = T - W;
     if (LSE) {  // query tiles count from the window's first query; the longest rows first
-      const int nq = (W + kRows - 1) / kRows;
+      head <<= p.pack;
       valid = t < nq;
-      r0 = wq0 + (nq - 1 - t) * kRows;
+      r0 = wq0 + (nq - 1 - t) * qtok;
       c0 = 0;
-      ncol = valid ? min(r0 + kRows, T) - 1 : 0;
-      ncol = ncol / kRows + 1;  // key tiles 0 .. that of the last row
-      steps = valid ? ncol : 0;
+      ncol = valid ? (min(r0 + qtok, T) - 1) / kRows + 1 : 0;  // key tiles 0 .. that of the last row
+      steps = ncol;
     } else {  // key tiles in order: the first are seen by the most queries
       valid = t * kRows < T;
       r0 = t * kRows;
-      const int nq = (W + kRows - 1) / kRows;
-      c0 = r0 > wq0 ? (r0 - wq0) / kRows : 0;  // earlier tiles end before the first key
+      c0 = r0 > wq0 ? (r0 - wq0) / qtok : 0;  // earlier tiles end before the first key
       ncol = nq - c0;
-      steps = valid ? ncol * (p.Hq / p.Hkv) : 0;
+      steps = valid ? ncol * ((p.Hq / p.Hkv) >> p.pack) : 0;
     }
   }
-  // step u: query head and first query (sums), or first key (lse) of the column tile
+  // step u: (first) query head and first query (sums), or first key (lse) of the column tile
   __device__ __forceinline__ void column(const WeightParams& p, int u, int& h, int& x0) const {
     if (LSE) {
       h = head / (p.Hq / p.Hkv);
       x0 = u * kRows;
     } else {
-      h = head * (p.Hq / p.Hkv) + u / ncol;
-      x0 = wq0 + (c0 + u % ncol) * kRows;
+      h = head * (p.Hq / p.Hkv) + (u / ncol << p.pack);
+      x0 = wq0 + (c0 + u % ncol) * (kRows >> p.pack);
     }
   }
 };
@@ -149,6 +155,7 @@ __global__ void __launch_bounds__(kWThreads, 2)
   const uint32_t base = (smem_u32(wsm_raw) + 1023u) & ~1023u;
   uint8_t* const gbase = wsm_raw + (base - smem_u32(wsm_raw));
   const uint32_t rank = cluster_rank(), nrank = cluster_size();
+  if (LSE) grid_release();
   WUnit<LSE> x;
   x.init(p, blockIdx.x / nrank);
   if (!x.valid) return;  // the whole cluster leaves
@@ -157,8 +164,9 @@ __global__ void __launch_bounds__(kWThreads, 2)
   const uint32_t bars = base + C::kOffBar;
   const uint32_t bar_a = bars;
   auto bar_bfull = [&](int s) { return bars + (1 + s) * 8; };
-  auto bar_bfree = [&](int s) { return bars + (1 + C::kStages + s) * 8; };
-  constexpr int kSB = 1 + 2 * C::kStages;
+  auto bar_bfree = [&](int s) { return bars + (1 + C::kStages1 + s) * 8; };
+  constexpr int kSB = 1 + 2 * C::kStages1;
+  const int stages = p.stages;
   auto bar_sfull = [&](int w) { return bars + (kSB + w) * 8; };
   auto bar_sfree = [&](int w) { return bars + (kSB + 2 + w) * 8; };
   auto bar_cfull = [&](int s) { return bars + (kSB + 4 + s) * 8; };
@@ -172,7 +180,7 @@ __global__ void __launch_bounds__(kWThreads, 2)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     mbar_init(bar_a, 1);
-    for (int s = 0; s < C::kStages; ++s) {
+    for (int s = 0; s < stages; ++s) {
       mbar_init(bar_bfull(s), 1);
       mbar_init(bar_bfree(s), 1);
     }
@@ -212,7 +220,7 @@ __global__ void __launch_bounds__(kWThreads, 2)
       tma_load_3d_e(base + C::kOffA + sl * kRows * 128, ma, bar_a, sl * 64, x.head, x.seq0 + x.r0);
     int n = 0;
     for (; n < nsteps; ++n) {
-      const int s = n % C::kStages, use = n / C::kStages;
+      const int s = n % stages, use = n / stages;
       if (use > 0 && !wwait(bar_bfree(s), (use - 1) & 1)) break;
       int h, x0;
       x.column(p, (int)rank + n * (int)nrank, h, x0);
@@ -224,8 +232,8 @@ __global__ void __launch_bounds__(kWThreads, 2)
     // every copy lands before the CTA can leave (only this warp arrives on these barriers)
     if (nsteps == 0 || *err) {
       mbar_wait_drain(bar_a, 0);
-      for (int s = 0; s < C::kStages && s < n; ++s)
-        mbar_wait_drain(bar_bfull(s), (uint32_t)(((n - 1 - s) / C::kStages) & 1));
+      for (int s = 0; s < stages && s < n; ++s)
+        mbar_wait_drain(bar_bfull(s), (uint32_t)(((n - 1 - s) / stages) & 1));
     }
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMA
@@ -233,10 +241,10 @@ __global__ void __launch_bounds__(kWThreads, 2)
     const uint64_t dA = smem_desc(base + C::kOffA, 16, 1024, kSwz128);
     bool ok = nsteps > 0 && wwait(bar_a, 0);
     for (int n = 0; ok && n < nsteps; ++n) {
-      const int s = n % C::kStages, w = n & 1;
+      const int s = n % stages, w = n & 1;
       // S block w last held tile n - 2; its warps have read it into registers
       if (n >= 2 && !wwait(bar_sfree(w), ((n >> 1) - 1) & 1)) break;
-      if (!wwait(bar_bfull(s), (n / C::kStages) & 1)) break;
+      if (!wwait(bar_bfull(s), (n / stages) & 1)) break;
       tc_fence_after();
       const uint64_t dB = smem_desc(base + C::kOffB + s * C::kTileBytes, 16, 1024, kSwz128);
 #pragma unroll
@@ -253,6 +261,7 @@ __global__ void __launch_bounds__(kWThreads, 2)
   } else if (warp < 4) {
     // ---------------------------------------------------------------- column normalisers
     if (!LSE) {
+      grid_wait();  // the lse may be the preceding launch's
       const int c = (warp - 2) * 64 + lane;  // and c + 32
       for (int n = 0; n < nsteps; ++n) {
         const int s = n % kColSlots, use = n / kColSlots;
@@ -263,8 +272,8 @@ __global__ void __launch_bounds__(kWThreads, 2)
         bool odd = false;
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          const int i = x0 + c + 32 * k;
-          const float z = i < x.T ? src[i] : INFINITY;
+          const int i = x0 + ((c + 32 * k) >> p.pack);
+          const float z = i < x.T ? src[((c + 32 * k) & ((1 << p.pack) - 1)) * p.ntok + i] : INFINITY;
           const bool fin = isfinite(z);  // a row that is not finite adds nothing
           odd |= !fin;
           col[s * kRows + c + 32 * k] = fin ? z * -1.4426950408889634f : -INFINITY;
@@ -279,10 +288,11 @@ __global__ void __launch_bounds__(kWThreads, 2)
     // ---------------------------------------------------------------- softmax warps
     const int w = (warp - 4) >> 2;                    // tile parity, S block
     const int r = (warp & 3) * 32 + lane;             // row = TMEM lane
-    const int row = x.r0 + r;                         // query or key position
+    const int row = x.r0 + (LSE ? r >> p.pack : r);   // query or key position
     const uint32_t tS = tmem + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)(w * kRows);
     const float c1 = p.scale_log2;
     const float2 c2 = make_float2(c1, c1);
+    const bool warp_rows = x.r0 + ((warp & 3) * 32 >> (LSE ? p.pack : 0)) < x.T;
     float total = 0.0f, comp = 0.0f;                  // sums: compensated total
     float mref = -INFINITY, l = 0.0f;                 // lse
     for (int n = w; n < nsteps; n += 2) {
@@ -293,7 +303,15 @@ __global__ void __launch_bounds__(kWThreads, 2)
       if (!mbar_wait(bar_sfull(w), (n >> 1) & 1, err)) break;
       __syncwarp();
       tc_fence_after();
-      if (LSE) {
+      // the S block is free for the tile after next once its last columns are in registers
+      auto release_s = [&] {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar_sfree(w));
+      };
+      if (!warp_rows) {  // no row of this warp exists: the tile only passes through
+        release_s();
+      } else if (LSE) {
         // keys behind the last row of the sequence are behind every valid row, too
         const bool masked = x0 + kRows - 1 > x.r0;
         const int nchunk = min(kRows, x.T - x0 + 31) >> 5;
@@ -303,6 +321,7 @@ __global__ void __launch_bounds__(kWThreads, 2)
           tmem_ld32(tS + 32 * ch, sr);
           tmem_wait_ld();
           tmem_reg_fence(sr);
+          if (ch == nchunk - 1) release_s();
           if (masked) {
             const int lim = row - (x0 + 32 * ch);  // columns 0 .. lim are visible
 #pragma unroll
@@ -334,7 +353,7 @@ __global__ void __launch_bounds__(kWThreads, 2)
         // nothing; where a tile has such columns they are selected away one by one, since
         // a score there may be anything
         const bool masked = x0 < x.r0 + kRows - 1 || flag[cs * 2] || flag[cs * 2 + 1];
-        const int nchunk = min(kRows, x.T - x0 + 31) >> 5;
+        const int nchunk = (min(kRows, (x.T - x0) << p.pack) + 31) >> 5;
         const float4* const nl = reinterpret_cast<const float4*>(col + cs * kRows);
         float2 a[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll 1
@@ -343,6 +362,7 @@ __global__ void __launch_bounds__(kWThreads, 2)
           tmem_ld32(tS + 32 * ch, sr);
           tmem_wait_ld();
           tmem_reg_fence(sr);
+          if (ch == nchunk - 1) release_s();
           if (!masked) {
 #pragma unroll
             for (int k = 0; k < 32; k += 4) {
@@ -355,7 +375,7 @@ __global__ void __launch_bounds__(kWThreads, 2)
               a[1] = __fadd2_rn(a[1], make_float2(ex2(e1.x), ex2(e1.y)));
             }
           } else {
-            const int lim = row - (x0 + 32 * ch);  // columns from lim on see the key
+            const int lim = ((row - x0) << p.pack) - 32 * ch;  // columns from lim on see the key
 #pragma unroll
             for (int k = 0; k < 32; k += 4) {
               const float4 z = nl[8 * ch + k / 4];
@@ -378,11 +398,9 @@ __global__ void __launch_bounds__(kWThreads, 2)
         comp = __fsub_rn(__fsub_rn(t, total), y);
         total = t;
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(bar_sfree(w));
-        if (!LSE) mbar_arrive(bar_cfree(cs));
+      if (!LSE) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar_cfree(cs));
       }
     }
     part = LSE ? make_float2(mref, l) : make_float2(total, 0.0f);
@@ -396,9 +414,9 @@ __global__ void __launch_bounds__(kWThreads, 2)
 
   // join the CTAs' rows, even tiles then odd ones of each rank
   if (nrank > 1) cluster_sync();
-  if (rank == 0 && threadIdx.x < kRows && x.r0 + (int)threadIdx.x < x.T) {
+  const int row = x.r0 + (LSE ? (int)threadIdx.x >> p.pack : (int)threadIdx.x);
+  if (rank == 0 && threadIdx.x < kRows && row < x.T) {
     const uint32_t red = base + C::kOffRed + threadIdx.x * 8;
-    const int row = x.r0 + threadIdx.x;
     float mm = -INFINITY, acc = 0.0f;
     if (LSE)
       for (uint32_t k = 0; k < nrank; ++k)
@@ -410,7 +428,7 @@ __global__ void __launch_bounds__(kWThreads, 2)
         else acc += v.x;
       }
     if (LSE)
-      p.lse[(long long)x.head * p.ntok + x.seq0 + row] = (mm + log2f(acc)) * 0.69314718055994531f;
+      p.lse[(long long)(x.head + (threadIdx.x & ((1 << p.pack) - 1))) * p.ntok + x.seq0 + row] = (mm + log2f(acc)) * 0.69314718055994531f;
     else
       p.weights[(long long)(x.seq0 + row) * p.Hkv + x.head] = acc;
   }
@@ -418,44 +436,33 @@ __global__ void __launch_bounds__(kWThreads, 2)
   if (nrank > 1) cluster_sync();  // a CTA's rows stay until rank 0 has read them
 }
 
-// CTAs per unit: as few as bring the longest unit near the mean load of the grid's 296
-// places (two per SM), so that a short stream of units still fills the GPU.
-int cluster_for(long long total, long long longest) {
-  const long long mean = total / 296 > 4 ? total / 296 : 4;
-  int c = 1;
-  while (c < 8 && (longest + c - 1) / c > mean) c *= 2;
-  return c;
-}
-
 template <int D, bool LSE>
-cudaError_t launch_weight_pass(const WeightParams& p, const WeightMaps& m, long long units, int cluster,
-                               cudaStream_t s) {
+cudaError_t launch_weight_pass(WeightParams p, const WeightMaps& m, bool overlap, cudaStream_t s) {
   using C = WCfg<D>;
-  cudaError_t e = cudaFuncSetAttribute(weight_kernel<D, LSE>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  const long long units = LSE ? p.lse_units : p.sum_units, longest = LSE ? p.lse_longest : p.sum_longest;
+  // CTAs per unit: as few as bring the longest unit near the mean load of the grid's 296
+  // places (two per SM), so that a short stream of units still fills the GPU
+  const long long steps = LSE ? p.lse_steps : p.sum_steps, mean = steps / 296 > 4 ? steps / 296 : 4;
+  int cluster = 1;
+  while (cluster < 8 && (longest + cluster - 1) / cluster > mean) cluster *= 2;
+  const long long ctas = units * cluster;
+  if (ctas > 0x7FFFFFFFll) return cudaErrorInvalidConfiguration;
+  // a grid of at most one CTA per SM has each alone: the deeper ring.  (Only 15 clusters of 8
+  // such CTAs fit the GPU at a time: a 16th, as a second wave, would double the time.)
+  p.stages = ctas <= 120 ? C::kStages1 : C::kStages2;
+  static SmemLimit limit;
+  cudaError_t e = limit.raise(weight_kernel<D, LSE>, C::smem(C::kStages1));
   if (e != cudaSuccess) return e;
-  if (units * cluster > 0x7FFFFFFFll) return cudaErrorInvalidConfiguration;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(units * cluster));
-  cfg.blockDim = dim3(kWThreads);
-  cfg.dynamicSmemBytes = C::kSmem;
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = (unsigned)cluster;
-  at[0].val.clusterDim.y = 1;
-  at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, weight_kernel<D, LSE>, p, m);
+  return launch_ex(weight_kernel<D, LSE>, dim3((unsigned)ctas), kWThreads, C::smem(p.stages), s, cluster, overlap, p, m);
 }
 
 template <int D>
 cudaError_t launch_weight_d(const WeightParams& p, const WeightMaps& m, cudaStream_t s) {
   if (!p.lse_given) {
-    cudaError_t e = launch_weight_pass<D, true>(p, m, p.lse_units, cluster_for(p.lse_steps, p.lse_longest), s);
+    cudaError_t e = launch_weight_pass<D, true>(p, m, false, s);
     if (e != cudaSuccess) return e;
   }
-  return launch_weight_pass<D, false>(p, m, p.sum_units, cluster_for(p.sum_steps, p.sum_longest), s);
+  return launch_weight_pass<D, false>(p, m, !p.lse_given, s);
 }
 
 }  // namespace
