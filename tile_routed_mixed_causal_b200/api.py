@@ -8,6 +8,9 @@ hybrid_attention_decode per step (token-level hybrid: INT4 tiles plus bf16 selec
 and recent tokens).
 ``HybridPrefillPlan``: quantize_qkv_tiles (K and V INT4 scales) ->
 hybrid_select_tokens -> hybrid_attention_prefill.
+``EvictingDecodePlan``: attention_weight_sums -> paged_cache_fill (once, over the prompt)
+-> paged_attention_decode per step, with paged_cache_evict whenever a row reaches its limit.
+``prompt_importance``: attention_weight_sums as the importance of a hybrid selection.
 Buffers are allocated once per plan; ``run``/``step`` only enqueue kernels.  The
 decode workspace is zero-filled once (the decode's arrival counters need that, and
 every step leaves them at zero).
@@ -136,3 +139,58 @@ class HybridPrefillPlan:
     def run(self, q, k, v, importance, out, lse=None, scale=None, stream=None):
         self.prepare(k, v, importance, stream)
         self.attend(q, k, v, out, lse, scale, stream)
+
+
+def prompt_importance(shape: L.Shape, q, k, n_queries: int = 64, lse=None, scale=None, stream=None):
+    """Accumulated attention weight of the prompt's keys, float32 [ntok, Hkv]: the importance
+    that hybrid_select_tokens and paged_cache_fill take.  n_queries: the last queries of each
+    sequence that count (0: all); lse: what a prefill wrote, or None to compute it."""
+    scale = 1.0 / math.sqrt(shape.d) if scale is None else scale
+    weights = torch.empty((shape.ntok, shape.Hkv), dtype=torch.float32, device=q.device)
+    given = lse is not None
+    if not given:
+        lse = torch.empty((shape.Hq, shape.ntok), dtype=torch.float32, device=q.device)
+    L.attention_weight_sums(shape, q, k, weights, lse, n_queries=n_queries, softmax_scale=scale,
+                            lse_given=given, stream=stream)
+    return weights
+
+
+class EvictingDecodePlan:
+    """Decoding over a bounded INT8 cache: every row keeps `keep` pages of its prompt and grows
+    to `limit` pages, then its tokens of least accumulated attention weight go until `keep`
+    pages are left (the last `recent` tokens always stay)."""
+
+    def __init__(self, shape: L.Shape, keep: int, limit: int, recent: int = 64, n_queries: int = 64,
+                 device="cuda"):
+        if not 1 <= keep < limit:
+            raise ValueError(f"need 1 <= keep < limit (got {keep}, {limit})")
+        self.shape, self.keep, self.limit = shape, keep, limit
+        self.recent, self.n_queries = recent, n_queries
+        # an eviction writes its `keep` pages beside the row's own
+        self.cache = L.PagedCache(shape.B, shape.Hq, shape.Hkv, shape.d, limit + keep, device=device)
+        self.rows = None        # [pages, tail] of each row, as the device has them
+
+    @property
+    def status(self):
+        return self.cache.status
+
+    def prefill(self, q, k, v, lse=None, scale=None, stream=None):
+        """Weigh the prompt's keys (by the last n_queries queries) and store what stays."""
+        w = prompt_importance(self.shape, q, k, self.n_queries, lse, scale, stream)
+        L.paged_cache_fill(self.cache, self.shape, k, v, keep=self.keep, recent=self.recent, weights=w,
+                           stream=stream)
+        cu = self.shape.cu_host
+        lens = [int(b) - int(a) for a, b in zip(cu, cu[1:])]
+        self.rows = [[min(t // L.TILE, self.keep), t % L.TILE] for t in lens]
+        return w
+
+    def step(self, q, k_new, v_new, out, scale=None, stream=None):
+        """One decoded token per row; rows that have no room for its page are cut first."""
+        scale = 1.0 / math.sqrt(self.shape.d) if scale is None else scale
+        if any(n >= self.limit and t == L.TILE - 1 for n, t in self.rows):
+            L.paged_cache_evict(self.cache, keep=self.keep, recent=self.recent, stream=stream)
+            for r in self.rows:
+                r[0] = min(r[0], self.keep)
+        L.paged_attention_decode(self.cache, q, k_new, v_new, out, softmax_scale=scale, stream=stream)
+        for r in self.rows:
+            r[0], r[1] = r[0] + (r[1] == L.TILE - 1), (r[1] + 1) % L.TILE
