@@ -66,6 +66,20 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// 16 columns of the warp's TMEM lanes, and the fence that keeps their reads behind the wait
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void reg_fence16(uint32_t (&r)[16]) {
+  asm volatile("" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                    "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]));
+}
+
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
@@ -309,44 +323,66 @@ __global__ void __launch_bounds__(kWThreads, 2)
         __syncwarp();
         if (lane == 0) mbar_arrive(bar_sfree(w));
       };
+      // a full tile: 16 columns at a time, unrolled, the next 16 on their way meanwhile
+      auto pipelined = [&](auto body) {
+        uint32_t ra[16], rb[16];
+        tmem_ld16(tS, ra);
+#pragma unroll
+        for (int c0 = 0; c0 < kRows; c0 += 32) {
+          tmem_wait_ld();
+          reg_fence16(ra);
+          tmem_ld16(tS + c0 + 16, rb);
+          body(c0, ra);
+          tmem_wait_ld();
+          reg_fence16(rb);
+          if (c0 + 32 < kRows) tmem_ld16(tS + c0 + 32, ra);
+          else release_s();
+          body(c0 + 16, rb);
+        }
+      };
       if (!warp_rows) {  // no row of this warp exists: the tile only passes through
         release_s();
       } else if (LSE) {
         // keys behind the last row of the sequence are behind every valid row, too
         const bool masked = x0 + kRows - 1 > x.r0;
         const int nchunk = min(kRows, x.T - x0 + 31) >> 5;
-#pragma unroll 1
-        for (int ch = 0; ch < nchunk; ++ch) {
-          uint32_t sr[32];
-          tmem_ld32(tS + 32 * ch, sr);
-          tmem_wait_ld();
-          tmem_reg_fence(sr);
-          if (ch == nchunk - 1) release_s();
-          if (masked) {
-            const int lim = row - (x0 + 32 * ch);  // columns 0 .. lim are visible
-#pragma unroll
-            for (int k = 0; k < 32; ++k) sr[k] = k <= lim ? sr[k] : 0xFF800000u;
-          }
+        auto add = [&](auto& sr) {  // these columns into the row's maximum and sum
+          constexpr int N = sizeof(sr) / 4;
           float mx[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) mx[k] = __uint_as_float(sr[k]);
 #pragma unroll
-          for (int k = 4; k < 32; ++k) mx[k & 3] = fmaxf(mx[k & 3], __uint_as_float(sr[k]));
+          for (int k = 4; k < N; ++k) mx[k & 3] = fmaxf(mx[k & 3], __uint_as_float(sr[k]));
           const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c1;
           if (mt > mref + kLseSlack || (mref == -INFINITY && mt > mref)) {
             l *= ex2(mref - mt);  // mref = -inf gives 0
             mref = mt;
           }
           const float nm = mref == -INFINITY ? 0.0f : -mref;
-          const float2 nm2 = make_float2(nm, nm);
           float2 a[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
-          for (int k = 0; k < 32; k += 2) {
-            const float2 e = __ffma2_rn(make_float2(__uint_as_float(sr[k]), __uint_as_float(sr[k + 1])), c2, nm2);
+          for (int k = 0; k < N; k += 2) {
+            const float2 e = __ffma2_rn(make_float2(__uint_as_float(sr[k]), __uint_as_float(sr[k + 1])), c2, make_float2(nm, nm));
             a[(k >> 1) & 1] = __fadd2_rn(a[(k >> 1) & 1], make_float2(ex2(e.x), ex2(e.y)));
           }
           const float2 s2 = __fadd2_rn(a[0], a[1]);
           l += s2.x + s2.y;
+        };
+        if (!masked && nchunk == 4) {
+          pipelined([&](int, uint32_t (&sr)[16]) { add(sr); });
+        } else {
+#pragma unroll 1
+          for (int ch = 0; ch < nchunk; ++ch) {
+            uint32_t sr[32];
+            tmem_ld32(tS + 32 * ch, sr);
+            tmem_wait_ld();
+            tmem_reg_fence(sr);
+            if (ch == nchunk - 1) release_s();
+            const int lim = row - (x0 + 32 * ch);  // columns 0 .. lim are visible
+#pragma unroll
+            for (int k = 0; k < 32; ++k) sr[k] = k <= lim ? sr[k] : 0xFF800000u;
+            add(sr);
+          }
         }
       } else {
         // queries before the key, past the window's end or without a finite lse add
@@ -356,17 +392,11 @@ __global__ void __launch_bounds__(kWThreads, 2)
         const int nchunk = (min(kRows, (x.T - x0) << p.pack) + 31) >> 5;
         const float4* const nl = reinterpret_cast<const float4*>(col + cs * kRows);
         float2 a[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-#pragma unroll 1
-        for (int ch = 0; ch < nchunk; ++ch) {
-          uint32_t sr[32];
-          tmem_ld32(tS + 32 * ch, sr);
-          tmem_wait_ld();
-          tmem_reg_fence(sr);
-          if (ch == nchunk - 1) release_s();
-          if (!masked) {
+        if (!masked && nchunk == 4) {
+          pipelined([&](int c0, uint32_t (&sr)[16]) {
 #pragma unroll
-            for (int k = 0; k < 32; k += 4) {
-              const float4 z = nl[8 * ch + k / 4];
+            for (int k = 0; k < 16; k += 4) {
+              const float4 z = nl[(c0 + k) / 4];
               const float2 e0 = __ffma2_rn(make_float2(__uint_as_float(sr[k]), __uint_as_float(sr[k + 1])), c2,
                                            make_float2(z.x, z.y));
               const float2 e1 = __ffma2_rn(make_float2(__uint_as_float(sr[k + 2]), __uint_as_float(sr[k + 3])), c2,
@@ -374,7 +404,15 @@ __global__ void __launch_bounds__(kWThreads, 2)
               a[0] = __fadd2_rn(a[0], make_float2(ex2(e0.x), ex2(e0.y)));
               a[1] = __fadd2_rn(a[1], make_float2(ex2(e1.x), ex2(e1.y)));
             }
-          } else {
+          });
+        } else {
+#pragma unroll 1
+          for (int ch = 0; ch < nchunk; ++ch) {
+            uint32_t sr[32];
+            tmem_ld32(tS + 32 * ch, sr);
+            tmem_wait_ld();
+            tmem_reg_fence(sr);
+            if (ch == nchunk - 1) release_s();
             const int lim = ((row - x0) << p.pack) - 32 * ch;  // columns from lim on see the key
 #pragma unroll
             for (int k = 0; k < 32; k += 4) {
