@@ -84,8 +84,12 @@ SUM_CASES = [
 ]
 
 
+# many heads to a KV head: a query tile of few tokens
+SUM_GROUPS = [(32, 1, 64, [77, 3], 2), (64, 2, 128, [40], 1), (128, 1, 64, [9, 200], 1), (96, 1, 128, [70], 3), (24, 1, 64, [130], 9)]
+
+
 @pytest.mark.parametrize("given", [False, True])
-@pytest.mark.parametrize("hq,hkv,d,lens,window", SUM_CASES, ids=str)
+@pytest.mark.parametrize("hq,hkv,d,lens,window", SUM_CASES + SUM_GROUPS, ids=str)
 def test_weight_sums(hq, hkv, d, lens, window, given):
     gen = _rng(len(lens) + 7 * window + d)
     cu = _cu(lens)
@@ -556,6 +560,43 @@ def test_evict_pages_of_zero_and_tiny_scales():
     tra.paged_cache_evict(cache, keep=3)
     ref.evict(3, 0)
     ref.same()
+
+
+def test_pages_past_32_bits():
+    """A pool of more than 2^31 bytes, its last pages in use: the same as in a small pool."""
+    rows, far = [(3, 63), (5, 10)], 270000
+    near, (q, kn, vn) = _filled(rows, 8, 2, 128, 8, seed=5)
+    n = near.n_pool
+    t = dict(near.t)
+    for name in ("k8", "v8", "sk", "sv"):
+        x = near[name]
+        t[name] = torch.zeros((far, *x.shape[1:]), dtype=x.dtype, device=DEV)
+        t[name][far - n:].copy_(x)
+    for name in ("state", "weight", "pos", "k_tail", "v_tail"):
+        t[name] = near[name].clone()
+    t["table"] = near["table"] + (far - n)
+    big = tra.PagedCache(2, 8, 2, 128, 8, tensors=t)
+    assert t["k8"].numel() > 2 ** 31
+    gen = _rng(2)
+    k, v = _normal(gen, 400, 2, 128), _normal(gen, 400, 2, 128)
+    shape = tra.Shape([0, 270, 400], 8, 2, 128)
+    for call in ("decode", "evict", "fill"):
+        outs = []
+        for c in (near, big):
+            if call == "decode":
+                outs.append(torch.empty_like(q))
+                tra.paged_attention_decode(c, q, kn, vn, outs[-1], softmax_scale=0.09)
+            elif call == "evict":
+                tra.paged_cache_evict(c, keep=2, recent=40)
+            else:
+                tra.paged_cache_fill(c, shape, k, v, keep=3)
+        if outs:
+            assert torch.equal(*outs)
+        assert int(near.status) == 0 and int(big.status) == 0
+        assert torch.equal(near["table"] + (far - n), big["table"])
+        for name in near.NAMES:
+            if name != "table":
+                assert torch.equal(near[name], big[name][-n:] if name in ("k8", "v8", "sk", "sv") else big[name]), (call, name)
 
 
 # ================================================================ states and pages out of range

@@ -644,7 +644,7 @@ __global__ void __launch_bounds__(kFinThreads, 8) paged_finish_kernel(const Page
     hl[h] = h < grp ? s_il[h] : 0.0f;
   }
   // (a batch of loads before its stores: the compiler cannot tell their arrays apart)
-  constexpr int kBatch = GS > 4 ? 2 : 4;
+  constexpr int kBatch = GS > 4 ? 4 : 8;
   for (int i0 = x * chunk + t; i0 < end; i0 += kBatch * kFinThreads) {
     float s[kBatch][GS], old[kBatch];
 #pragma unroll
