@@ -20,7 +20,10 @@
 // warps 2 and 3 stage the columns' normalisers (sums only), warps 4-7 and 8-11 take the
 // even and the odd tiles, one S block of TMEM each.
 // Sums run in fp32: within a tile over four chains, tile sums with a compensated add, so
-// that the error does not grow with the number of tiles.
+// that the error does not grow with the number of tiles.  Over a caller's lse the scores are
+// held closer: the scale in two parts, and the channels of every other tile multiplied in
+// reverse, so that the tensor core's truncation (largest where the large products come
+// first) has the same mean for every head and the scale can carry it.
 // Where there are few units a cluster of up to 8 CTAs shares one (every C-th tile each)
 // and joins the partial rows over distributed shared memory in rank order: the same call
 // gives the same bits.
@@ -113,6 +116,8 @@ __device__ __forceinline__ void mma_bf16_e(uint32_t d_tmem, uint64_t a, uint64_t
       : "memory");
 }
 
+enum WeightPass { kPassLse, kPassSums, kPassGiven };  // kPassGiven: sums over a caller's lse
+
 // One unit and the tiles of its stream that this CTA takes.
 template <bool LSE>
 struct WUnit {
@@ -161,10 +166,11 @@ struct WUnit {
   }
 };
 
-template <int D, bool LSE>
+template <int D, WeightPass PASS>
 __global__ void __launch_bounds__(kWThreads, 2)
     weight_kernel(const __grid_constant__ WeightParams p, const __grid_constant__ WeightMaps m) {
   using C = WCfg<D>;
+  constexpr bool LSE = PASS == kPassLse, GIVEN = PASS == kPassGiven;
   extern __shared__ uint8_t wsm_raw[];
   const uint32_t base = (smem_u32(wsm_raw) + 1023u) & ~1023u;
   uint8_t* const gbase = wsm_raw + (base - smem_u32(wsm_raw));
@@ -262,9 +268,11 @@ __global__ void __launch_bounds__(kWThreads, 2)
       tc_fence_after();
       const uint64_t dB = smem_desc(base + C::kOffB + s * C::kTileBytes, 16, 1024, kSwz128);
 #pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk)  // 16 channels: 32 bytes within a 64-channel slab of 16 KB
-        mma_bf16_e(tmem + w * kRows, dA + (kk >> 2) * 1024 + (kk & 3) * 2, dB + (kk >> 2) * 1024 + (kk & 3) * 2,
-                   kId, kk > 0 ? 1u : 0u);
+      for (int i = 0; i < D / 16; ++i) {  // 16 channels: 32 bytes within a 64-channel slab of 16 KB
+        const int kk = GIVEN && (n & 1) ? D / 16 - 1 - i : i;
+        const uint32_t off = (kk >> 2) * 1024 + (kk & 3) * 2;
+        mma_bf16_e(tmem + w * kRows, dA + off, dB + off, kId, i > 0 ? 1u : 0u);
+      }
       mma_commit_e(bar_bfree(s));
       mma_commit_e(bar_sfull(w));
     }
@@ -305,7 +313,7 @@ __global__ void __launch_bounds__(kWThreads, 2)
     const int row = x.r0 + (LSE ? r >> p.pack : r);   // query or key position
     const uint32_t tS = tmem + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)(w * kRows);
     const float c1 = p.scale_log2;
-    const float2 c2 = make_float2(c1, c1);
+    const float2 c2 = make_float2(c1, c1), c2l = make_float2(p.scale_low, p.scale_low);
     const bool warp_rows = x.r0 + ((warp & 3) * 32 >> (LSE ? p.pack : 0)) < x.T;
     float total = 0.0f, comp = 0.0f;                  // sums: compensated total
     float mref = -INFINITY, l = 0.0f;                 // lse
@@ -397,10 +405,13 @@ __global__ void __launch_bounds__(kWThreads, 2)
 #pragma unroll
             for (int k = 0; k < 16; k += 4) {
               const float4 z = nl[(c0 + k) / 4];
-              const float2 e0 = __ffma2_rn(make_float2(__uint_as_float(sr[k]), __uint_as_float(sr[k + 1])), c2,
-                                           make_float2(z.x, z.y));
-              const float2 e1 = __ffma2_rn(make_float2(__uint_as_float(sr[k + 2]), __uint_as_float(sr[k + 3])), c2,
-                                           make_float2(z.z, z.w));
+              const float2 s0 = make_float2(__uint_as_float(sr[k]), __uint_as_float(sr[k + 1]));
+              const float2 s1 = make_float2(__uint_as_float(sr[k + 2]), __uint_as_float(sr[k + 3]));
+              float2 e0 = __ffma2_rn(s0, c2, make_float2(z.x, z.y)), e1 = __ffma2_rn(s1, c2, make_float2(z.z, z.w));
+              if (GIVEN) {
+                e0 = __ffma2_rn(s0, c2l, e0);
+                e1 = __ffma2_rn(s1, c2l, e1);
+              }
               a[0] = __fadd2_rn(a[0], make_float2(ex2(e0.x), ex2(e0.y)));
               a[1] = __fadd2_rn(a[1], make_float2(ex2(e1.x), ex2(e1.y)));
             }
@@ -421,7 +432,8 @@ __global__ void __launch_bounds__(kWThreads, 2)
               float e[4];
 #pragma unroll
               for (int y = 0; y < 4; ++y) {
-                e[y] = ex2(fmaf(__uint_as_float(sr[k + y]), c1, zz[y]));
+                const float sy = __uint_as_float(sr[k + y]), x = fmaf(sy, c1, zz[y]);
+                e[y] = ex2(GIVEN ? fmaf(sy, p.scale_low, x) : x);
                 if (k + y < lim || zz[y] == -INFINITY) e[y] = 0.0f;
               }
               a[0] = __fadd2_rn(a[0], make_float2(e[0], e[1]));
@@ -474,9 +486,10 @@ __global__ void __launch_bounds__(kWThreads, 2)
   if (nrank > 1) cluster_sync();  // a CTA's rows stay until rank 0 has read them
 }
 
-template <int D, bool LSE>
+template <int D, WeightPass PASS>
 cudaError_t launch_weight_pass(WeightParams p, const WeightMaps& m, bool overlap, cudaStream_t s) {
   using C = WCfg<D>;
+  constexpr bool LSE = PASS == kPassLse;
   const long long units = LSE ? p.lse_units : p.sum_units, longest = LSE ? p.lse_longest : p.sum_longest;
   // CTAs per unit: as few as bring the longest unit near the mean load of the grid's 296
   // places (two per SM), so that a short stream of units still fills the GPU
@@ -489,18 +502,16 @@ cudaError_t launch_weight_pass(WeightParams p, const WeightMaps& m, bool overlap
   // such CTAs fit the GPU at a time: a 16th, as a second wave, would double the time.)
   p.stages = ctas <= 120 ? C::kStages1 : C::kStages2;
   static SmemLimit limit;
-  cudaError_t e = limit.raise(weight_kernel<D, LSE>, C::smem(C::kStages1));
+  cudaError_t e = limit.raise(weight_kernel<D, PASS>, C::smem(C::kStages1));
   if (e != cudaSuccess) return e;
-  return launch_ex(weight_kernel<D, LSE>, dim3((unsigned)ctas), kWThreads, C::smem(p.stages), s, cluster, overlap, p, m);
+  return launch_ex(weight_kernel<D, PASS>, dim3((unsigned)ctas), kWThreads, C::smem(p.stages), s, cluster, overlap, p, m);
 }
 
 template <int D>
 cudaError_t launch_weight_d(const WeightParams& p, const WeightMaps& m, cudaStream_t s) {
-  if (!p.lse_given) {
-    cudaError_t e = launch_weight_pass<D, true>(p, m, false, s);
-    if (e != cudaSuccess) return e;
-  }
-  return launch_weight_pass<D, false>(p, m, !p.lse_given, s);
+  if (p.lse_given) return launch_weight_pass<D, kPassGiven>(p, m, false, s);
+  cudaError_t e = launch_weight_pass<D, kPassLse>(p, m, false, s);
+  return e != cudaSuccess ? e : launch_weight_pass<D, kPassSums>(p, m, true, s);
 }
 
 }  // namespace
