@@ -418,6 +418,28 @@ def test_fill_values_at_the_borders():
     ref.same()
 
 
+@pytest.mark.parametrize("exponent", [0, 57, -60, -91, -92, -94, -110])
+def test_fill_every_quotient(exponent):
+    """Every quotient of a bf16 value and a largest value that does not round to zero: page i has the
+    largest value (128 + i) 2^exponent and all X 2^-j below it, both signs."""
+    x = torch.arange(128, 256, dtype=torch.float64)
+    vals = torch.cat([x * 2.0 ** -j for j in range(11)])
+    pages = []
+    for a in range(128, 256):
+        v = vals[vals <= a]
+        v = torch.cat([v, -v, torch.tensor([float(a)])])
+        pages.append(torch.cat([v, torch.zeros(TILE * 64 - len(v), dtype=torch.float64)]).view(TILE, 64))
+    k = (torch.cat(pages) * 2.0 ** exponent).to(torch.bfloat16)
+    assert torch.equal(k.double(), torch.cat(pages) * 2.0 ** exponent)
+    k = k.to(DEV)[:, None].contiguous()
+    T = k.shape[0]
+    cache, _ = _filled([(-1, 0)], 1, 1, 64, 128, seed=6)
+    ref = Mirror(cache)
+    tra.paged_cache_fill(cache, tra.Shape([0, T], 1, 1, 64), k, -k, keep=128)
+    ref.fill([0, T], k, -k, None, 128, 0)
+    ref.same()
+
+
 # ================================================================ decode
 STEPS = [
     # heads, d, cap, rows (pages, tail)

@@ -316,6 +316,26 @@ struct CodeRange {
   }
 };
 
+// N values times the factor one side (fa) and the other (fb): fa's rounded products in the
+// low bits of z; returns how many values' two products differ.
+template <int N>
+__device__ __forceinline__ float round_codes(const float (&x)[N], float fa, float fb, float (&z)[N]) {
+  float2 apart = make_float2(0.0f, 0.0f);
+#pragma unroll
+  for (int j = 0; j < N; j += 2) {
+    const float2 v = make_float2(x[j], x[j + 1]);
+    const float2 za = __ffma2_rn(v, make_float2(fa, fa), make_float2(kRoundMagic, kRoundMagic));
+    const float2 zb = __ffma2_rn(v, make_float2(-fb, -fb), make_float2(-kRoundMagic, -kRoundMagic));
+    const float2 e = __fadd2_rn(za, zb);  // 0 or +-1
+    apart = __ffma2_rn(e, e, apart);
+    z[j] = za.x;
+    z[j + 1] = za.y;
+  }
+  return apart.x + apart.y;
+}
+
+// Rare, and kept out of the loops: inlined and unrolled, the divisions overflowed the
+// instruction cache (evict of 16 x 32K: 570 us).
 __device__ __noinline__ uint32_t code_exact(float s, float f, float sn) {
   return (uint32_t)quant_code(__fmul_rn(s, f), sn, 127);
 }

@@ -14,15 +14,23 @@ __device__ __forceinline__ PagedRow paged_row(int4 st, int cap) {
   return st.x <= cap && st.y >= 0 && st.y < kTile ? kRowOk : kRowBad;
 }
 
-// Rounding a quotient to its code without a division per value.  The definition's quotient
-// fl32(x / s) (evict: fl32(fl32(s' code) / s)) and a value times a rounded factor 1 / s
-// (s' / s, from an approximate reciprocal) differ by less than 7 * 2^-24 of the value.  So each value is
-// multiplied by two factors, 2^-21 above and below the rounded one: the definition's
-// quotient lies between the products, and where both round to the same integer, so does
-// it (rounding is monotone).  Values that straddle a half take the division: about one in
-// 25,000, and the exact halves (half the block's largest value: 63.5).
-// Adding 1.5 * 2^23 in the same fma rounds the exact product to the nearest integer, ties
-// to even, and leaves its two's complement in the low bits.
+// Rounding quotients to codes without a division per value.  Adding 1.5 * 2^23 to a product
+// in one fma rounds the exact product to the nearest integer, ties to even, and leaves its
+// two's complement in the low bits.  Which factor rounds as the definition's division does:
+//
+// bf16 values (fill, and a tail that becomes a page): rne(fl32(x / s)) with s = fl32(amax / 127).
+// With x = X 2^-j and amax = A (integers of 8 bits, up to a common power of two), the quotient
+// y = 127 X / (A 2^j) misses a half (2 n + 1) / 2 by |254 X - A (2 n + 1) 2^j| / (A 2^(j+1)): by
+// nothing, or by at least 1 / (254 X) > 2^-16 of y, while the roundings of s, of a factor near 1 / s and
+// of the quotient are below 2^-20 of y.  Exact halves: 127 divides A (2 n + 1), so y is 63.5
+// (|x| = amax / 2) or A is 2 * 127, where s is a power of two and every step exact.  So the
+// factor is 1 / s, nudged to the side to which the definition rounds 63.5.
+//
+// codes of another page (evict): rne(fl32(fl32(s' c) / s)).  This quotient and c times a rounded
+// s' / s (from an approximate reciprocal) differ by less than 7 * 2^-24 of the value.  So each
+// code is multiplied by two factors, 2^-21 above and below: the definition's quotient lies between
+// the products, and where both round to the same integer, so does it (rounding is monotone).
+// Chunks with a code that straddles a half take that code's division.
 constexpr float kRoundMagic = 12582912.0f;
 constexpr float kAbove = 1.0f + 0x1p-21f, kBelow = 1.0f - 0x1p-21f;
 // below this scale quotients of denormal values lose the bound above: always divide
@@ -41,42 +49,22 @@ __device__ __forceinline__ uint32_t low_bytes(float a, float b, float c, float d
                      __byte_perm(__float_as_uint(c), __float_as_uint(d), 0x0040), 0x5410);
 }
 
-// N values times the factor one side (fa) and the other (fb): fa's rounded products in the
-// low bits of z; returns how many values' two products differ.
-template <int N>
-__device__ __forceinline__ float round_codes(const float (&x)[N], float fa, float fb, float (&z)[N]) {
-  float2 apart = make_float2(0.0f, 0.0f);
-#pragma unroll
-  for (int j = 0; j < N; j += 2) {
-    const float2 v = make_float2(x[j], x[j + 1]);
-    const float2 za = __ffma2_rn(v, make_float2(fa, fa), make_float2(kRoundMagic, kRoundMagic));
-    const float2 zb = __ffma2_rn(v, make_float2(-fb, -fb), make_float2(-kRoundMagic, -kRoundMagic));
-    const float2 e = __fadd2_rn(za, zb);  // 0 or +-1
-    apart = __ffma2_rn(e, e, apart);
-    z[j] = za.x;
-    z[j + 1] = za.y;
-  }
-  return apart.x + apart.y;
-}
-
-// The scale of a block of bf16 values and the factors that round its quotients: 63.5, the one
-// quotient that bf16 values hit often (any |x| that is half the largest), is divided once, and
-// `fa` is the side that rounds it as the definition does.
+// The scale of a block of bf16 values, and the factor that rounds its quotients.
 struct BlockScale {
-  float s, fa, fb;
-  uint32_t half;  // half the largest value, twice
+  float s, f;
+  bool divide;  // scales so small that quotients of denormal values lose the bounds above
   __device__ __forceinline__ explicit BlockScale(float amax) {
     s = __fdiv_rn(amax, 127.0f);
-    const float r = recip(s);
-    const bool up = quant_code(amax * 0.5f, s, 127) == 64;
-    fa = r * (up ? kAbove : kBelow);
-    fb = r * (up ? kBelow : kAbove);
-    half = (__float_as_uint(amax * 0.5f) >> 16) * 0x10001u;
+    divide = s < kSmallScale;
+    f = recip(s);
+    if ((__float_as_uint(s) & 0x007FFFFFu) == 0)
+      f = __uint_as_float(0x7F000000u - __float_as_uint(s));  // a power of two: its exact reciprocal
+    else
+      f *= quant_code(amax * 0.5f, s, 127) == 64 ? kAbove : kBelow;
   }
 };
 
-// Codes of eight bf16 values by the definition.  Rare, and kept out of the loops: inlined and
-// unrolled, the divisions overflowed the instruction cache (evict of 16 x 32K: 570 us).
+// Codes of eight bf16 values by the definition.
 static __device__ __noinline__ uint2 codes8_exact(uint4 v, float s) {
   uint2 o = make_uint2(0u, 0u);
 #pragma unroll 1
@@ -91,22 +79,14 @@ static __device__ __noinline__ uint2 codes8_exact(uint4 v, float s) {
 
 // Codes of eight bf16 values (16 bytes).
 __device__ __forceinline__ uint2 codes8(uint4 v, const BlockScale& b) {
+  if (b.divide) return codes8_exact(v, b.s);
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-  float x[8], z[8];
-  __nv_bfloat162 halves = __floats2bfloat162_rn(0.0f, 0.0f);
+  float2 z[4];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    x[2 * j] = __uint_as_float(w[j] << 16);
-    x[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
-    const uint32_t mag = w[j] & 0x7FFF7FFFu;
-    halves = __hadd2(halves, __heq2(*reinterpret_cast<const __nv_bfloat162*>(&mag),
-                                    *reinterpret_cast<const __nv_bfloat162*>(&b.half)));
-  }
-  const float apart = round_codes<8>(x, b.fa, b.fb, z);
-  // (a NaN, from a scale of zero, compares unequal)
-  if (apart == __low2float(halves) + __high2float(halves) && b.s >= kSmallScale)
-    return make_uint2(low_bytes(z[0], z[1], z[2], z[3]), low_bytes(z[4], z[5], z[6], z[7]));
-  return codes8_exact(v, b.s);
+  for (int j = 0; j < 4; ++j)
+    z[j] = __ffma2_rn(make_float2(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xFFFF0000u)),
+                      make_float2(b.f, b.f), make_float2(kRoundMagic, kRoundMagic));
+  return make_uint2(low_bytes(z[0].x, z[0].y, z[1].x, z[1].y), low_bytes(z[2].x, z[2].y, z[3].x, z[3].y));
 }
 
 // largest |x| of eight bf16 values
