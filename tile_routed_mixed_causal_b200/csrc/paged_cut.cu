@@ -103,23 +103,8 @@ __global__ void __launch_bounds__(kSelThreads) paged_select_kernel(const PagedCu
   int first = !FILL || p.imp ? min(max(total - p.recent, body - m), body) : body - m;
   if (m == body) first = 0;
   int32_t* const out = p.ws_src + (long long)row * c.cap * kTile;
-  int32_t* const out_row = FILL ? nullptr : p.ws_row + (long long)row * c.cap * kTile;
-  // evict: the rows of the codes that hold tokens j .., a page at a time
-  const int32_t* const table = c.table + (long long)row * c.cap;
-  auto page_row = [&](int j) -> int {
-    if (FILL || j >= body) return 0;
-    const int page = table[j / kTile];
-    if (page < 0 || page >= c.n_pool) {
-      atomicOr(p.status, TRA_DEV_BAD_CACHE);
-      return j % kTile;
-    }
-    return page * kTile + j % kTile;
-  };
   if (body - first == m) {
-    for (int i = t; i < m; i += kSelThreads) {
-      out[i] = first + i;
-      if (!FILL) out_row[i] = page_row(first + i);
-    }
+    for (int i = t; i < m; i += kSelThreads) out[i] = first + i;
     return;
   }
 
@@ -241,7 +226,6 @@ __global__ void __launch_bounds__(kSelThreads) paged_select_kernel(const PagedCu
     __syncthreads();
     for (int i = 0; i < chunks; ++i) {
       const int j = s0 + (i * kSelThreads + t) * 4;
-      const int prow = page_row(j);
       const uint4 k4 = key4(j);
       const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
       uint32_t both = 0;
@@ -259,11 +243,7 @@ __global__ void __launch_bounds__(kSelThreads) paged_select_kernel(const PagedCu
 #pragma unroll
       for (int y = 0; y < 4; ++y) {
         const bool gt = k[y] > kth, eq = k[y] == kth;
-        if (gt || (eq && e < ties)) {
-          const uint32_t at = a + min(e, ties);
-          out[at] = j + y;
-          if (!FILL) out_row[at] = prow + y;
-        }
+        if (gt || (eq && e < ties)) out[a + min(e, ties)] = j + y;
         a += gt;
         e += eq;
       }
@@ -453,10 +433,20 @@ __global__ void __launch_bounds__(PageCfg<D, FILL>::kThreads, FILL ? 4 : 7)
   // the thread's survivors of page i: their rows' sources and, for t < 64, token t
   auto sources = [&](int i, int (&src)[C::kRowsEach], int& tok) {
     const int32_t* const s = p.ws_src + ((long long)row * c.cap + i) * kTile;
-    const int32_t* const r = FILL ? s : p.ws_row + ((long long)row * c.cap + i) * kTile;
 #pragma unroll
-    for (int y = 0; y < C::kRowsEach; ++y) src[y] = r[r0 + y * C::kRowStep];
+    for (int y = 0; y < C::kRowsEach; ++y) src[y] = s[r0 + y * C::kRowStep];
     tok = t < kTile ? s[t] : 0;
+    if (!FILL) {  // evict: the rows of the codes
+      bool bad = false;
+#pragma unroll
+      for (int y = 0; y < C::kRowsEach; ++y) {
+        const int page = table[src[y] / kTile];
+        const bool in = page >= 0 && page < c.n_pool;
+        bad |= !in;
+        src[y] = (in ? page * kTile : 0) + src[y] % kTile;
+      }
+      if (bad) atomicOr(p.status, TRA_DEV_BAD_CACHE);
+    }
   };
   auto fetch = [&](int i, const int (&src)[C::kRowsEach], int tok, PageRows<D, FILL>& x) {
 #pragma unroll

@@ -737,8 +737,7 @@ PagedLayout paged_layout(const tra_paged_cache& c) {
   l.scores = l.o + up(slots * grp * c.d * 4);
   const size_t step_end = l.scores + up(rows * (c.cap + 1) * kTile * paged_score_stride((int)grp) * 4);
   l.src = head;
-  l.row = l.src + up(rows * c.cap * kTile * 4);
-  l.dst = l.row + up(rows * c.cap * kTile * 4);
+  l.dst = l.src + up(rows * c.cap * kTile * 4);
   l.weight = l.dst + up(rows * c.cap * 4);
   l.pos = l.weight + up(rows * (c.cap + 1) * kTile * 4);
   const size_t cut_end = l.pos + up(rows * (c.cap + 1) * kTile * 4);

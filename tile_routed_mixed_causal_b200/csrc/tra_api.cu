@@ -915,7 +915,6 @@ tra_status paged_cache_fill(const tra_paged_cache* cache, const tra_shape* shape
   p.status = status_dev;
   p.ws_state = reinterpret_cast<int4*>(ws + lay.state);
   p.ws_src = reinterpret_cast<int32_t*>(ws + lay.src);
-  p.ws_row = reinterpret_cast<int32_t*>(ws + lay.row);
   p.ws_dst = reinterpret_cast<int32_t*>(ws + lay.dst);
   cudaError_t e = tra::launch_paged_fill(p, reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "paged fill launch");
@@ -994,7 +993,6 @@ tra_status paged_cache_evict(const tra_paged_cache* cache, int32_t keep, int32_t
   p.status = status_dev;
   p.ws_state = reinterpret_cast<int4*>(ws + lay.state);
   p.ws_src = reinterpret_cast<int32_t*>(ws + lay.src);
-  p.ws_row = reinterpret_cast<int32_t*>(ws + lay.row);
   p.ws_dst = reinterpret_cast<int32_t*>(ws + lay.dst);
   cudaError_t e = tra::launch_paged_evict(p, reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "paged evict launch");

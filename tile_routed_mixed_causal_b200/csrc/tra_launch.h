@@ -245,12 +245,11 @@ struct PagedCutParams {
   int in_place;          // evict: weight_out and pos_out are the workspace's, settled afterwards
   int4* ws_state;        // [B] what the selection found (paged_write_kernel)
   int32_t* ws_src;       // [B][Hkv][cap * 64] the survivors' tokens, ascending
-  int32_t* ws_row;       // evict: [B][Hkv][cap * 64] their rows in the codes (page * 64 + slot)
   int32_t* ws_dst;       // [B][Hkv][cap] scratch of the settling
 };
 
 struct PagedLayout {     // byte offsets in the workspace
-  size_t state, ml, o, scores, info, src, row, dst, weight, pos, total;
+  size_t state, ml, o, scores, info, src, dst, weight, pos, total;
 };
 PagedLayout paged_layout(const tra_paged_cache& c);
 // floats per token in the score array: the group's heads, an even number above one
