@@ -382,7 +382,7 @@ TRA_API int32_t tra_hybrid_capacity(const tra_shape* shape, double frac);
 /*
  * hybrid_select_tokens -- the high-precision side of the hybrid cache.  importance:
  * device float [ntok][Hkv] (finite), one score per key position and KV head (the
- * signal that marks "vertical lines"; synthetic in this library's tests);
+ * signal that marks "vertical lines": attention_weight_sums computes one);
  * k, v: device bf16 [ntok][Hkv][d].  Writes every array of *hy (layouts above).
  * TRA_ERR_INVALID for bad pointers, frac outside [0, 1], window < 0;
  * TRA_ERR_BUFFER if hy->cap is below tra_hybrid_capacity.
@@ -452,7 +452,8 @@ TRA_API tra_status hybrid_attention_prefill(const tra_shape* shape, const tra_hy
  * is read (the lse a prefill wrote; a row that is not finite adds nothing), otherwise the
  * window's rows are computed from q and k (dense causal) and written, and the other rows
  * are left as they were.  Products of bf16 inputs are summed in fp32, as are the weights,
- * in a fixed order: the same call gives the same bits.  status_dev as in the prefill.
+ * in a fixed order: the same call gives the same bits.  q and k finite; nothing of another
+ * sequence or of a masked pair reaches a result.  status_dev as in the prefill.
  */
 TRA_API tra_status attention_weight_sums(const tra_shape* shape, const uint16_t* q, const uint16_t* k,
                                          int32_t n_queries, float softmax_scale, float* lse,

@@ -5,13 +5,17 @@
 // staged once in shared memory, protected tokens as the largest; a radix select (three digits
 // of 11, 11 and 10 bits) finds the last key that survives, and one ascending pass writes the
 // survivors' indices at their ranks, ties taken in order.  Bound by latency: a dozen
-// block-wide steps, so it writes nothing but the indices.
+// block-wide steps, so it writes nothing but the indices.  32K tokens: 21 us, 26 us where the
+// weights of all heads lie side by side (fill); 4K: 6 us.
 //
 // Pages, one CTA per (up to four pages, K or V, KV head, sequence): 64 gathered rows are held in
 // registers while their maximum is reduced, then written as codes, the next page's rows
 // already on their way; the K part moves the tokens' weights, the V part their positions.
 // One read and one write of what survives: bound by memory.  (Survivors are single rows of
 // d values anywhere in the source, 64 to 256 bytes each: every access is whole sectors.)
+// 16 x 32K tokens: fill to 8K per head 143 us (5.7 TB/s), evict to 16K 300 us (3.7 TB/s; 11
+// instructions per code bound it).  K and V apart, and 32 values or 64 codes per thread, leave
+// room for enough CTAs; half or double the threads cost evict 20 %.
 //
 // A row that is cut in place gets its weights and positions through the workspace and a
 // third kernel, since pages are written in any order.

@@ -16,6 +16,9 @@
 // The scores live in TMEM and registers only.  Per element the kernel needs one product
 // column of the tensor cores (d multiply-adds, 4096 per SM and cycle) and one exponential
 // (16 per SM and cycle), so for d <= 128 the exponentials bound it.
+// (32 heads x 32K tokens, all queries, lse given: 5.7 ms, the exponential unit 80 % busy at the
+// 1 kW power limit.  Part of the exponentials as a polynomial on the FMA pipe: within 3 %.  Twice
+// the softmax warps: 6 % slower.)
 // Roles (384 threads, two CTAs per SM): warp 0 copies tiles (TMA), warp 1 issues the MMAs,
 // warps 2 and 3 stage the columns' normalisers (sums only), warps 4-7 and 8-11 take the
 // even and the odd tiles, one S block of TMEM each.
