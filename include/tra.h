@@ -526,7 +526,8 @@ TRA_API tra_status paged_cache_fill(const tra_paged_cache* cache, const tra_shap
  * what it writes to the tail, to pos and to the free page lies behind the old state's
  * tokens.  state_out and weight_out are the cache's own arrays or do not overlap them.
  * A row whose tail would fill with no free page left sets TRA_DEV_CACHE_FULL, keeps its
- * state and leaves its output, tail and weights untouched.
+ * state and weights (state_out and weight_out receive them as they are) and leaves its
+ * output and tail untouched.
  */
 TRA_API tra_status paged_attention_decode(const tra_paged_cache* cache, const uint16_t* q,
                                           const uint16_t* k_new, const uint16_t* v_new,

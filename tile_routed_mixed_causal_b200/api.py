@@ -186,6 +186,8 @@ class EvictingDecodePlan:
 
     def step(self, q, k_new, v_new, out, scale=None, stream=None):
         """One decoded token per row; rows that have no room for its page are cut first."""
+        if self.rows is None:
+            raise RuntimeError("step() needs a prompt: call prefill() first")
         scale = 1.0 / math.sqrt(self.shape.d) if scale is None else scale
         if any(n >= self.limit and t == L.TILE - 1 for n, t in self.rows):
             L.paged_cache_evict(self.cache, keep=self.keep, recent=self.recent, stream=stream)

@@ -181,9 +181,13 @@ __global__ void __launch_bounds__(kStepThreads, 2)
   const int grp = c.Hq / c.Hkv;
 
   grid_release();
+  if (t == 32 * kCons) {
+    prefetch_map(&m.k8);
+    prefetch_map(&m.v8);
+  }
   if (t == 0) {
     for (int s = 0; s < C::kStages; ++s) {
-      mbar_init(bar_full + s * 8, 1);
+      mbar_init(bar_full + s * 8, 2);  // the copies' bytes, and the scales
       mbar_init(bar_empty + s * 8, 1);
     }
     *err = 0;
@@ -220,7 +224,7 @@ __global__ void __launch_bounds__(kStepThreads, 2)
 
   if (warp == kCons) {
     // ---------------------------------------------------------------- producer
-    int issued = 0;
+    int issued = 0, scaled = 0, first = 0;  // pages copied, pages with scales, first of the batch
     bool bad = false;
     uint64_t pol;
     asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(pol));
@@ -244,27 +248,39 @@ __global__ void __launch_bounds__(kStepThreads, 2)
         const float2 sg = sc;
         if (i + 32 < end) fetch(i + 32);
         const int cnt = min(32, end - i);
+        // the first stages' copies start on the page numbers alone; their scales, another load
+        // later, follow together, and from then on each page's with its copy
         for (int k = 0; k < cnt; ++k, ++issued) {
           const int s = issued % C::kStages, use = issued / C::kStages;
           if (use > 0 && !__all_sync(0xffffffffu, mbar_wait(bar_empty + s * 8, (use - 1) & 1, err))) return false;
           const int pk = __shfl_sync(0xffffffffu, pg, k);
-          const float sx = __shfl_sync(0xffffffffu, sg.x, k), sy = __shfl_sync(0xffffffffu, sg.y, k);
           if (lane == 0) {
-            scale[s] = make_float2(sx, sy);
             const uint32_t dst = base + s * C::kStageBytes;
             mbar_arrive_expect_tx(bar_full + s * 8, C::kStageBytes);
             tma_load_page(dst, &m.k8, bar_full + s * 8, pk * kTile, pol);
             tma_load_page(dst + C::kTileBytes, &m.v8, bar_full + s * 8, pk * kTile, pol);
           }
+          if (issued < C::kStages - 1 && k < cnt - 1) continue;
+          for (; scaled - first <= k; ++scaled) {
+            const float sx = __shfl_sync(0xffffffffu, sg.x, scaled - first), sy = __shfl_sync(0xffffffffu, sg.y, scaled - first);
+            if (lane == 0) {
+              scale[scaled % C::kStages] = make_float2(sx, sy);
+              mbar_arrive(bar_full + scaled % C::kStages * 8);
+            }
+          }
         }
+        first = scaled;
       }
       return true;
     });
     if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(p.status, TRA_DEV_BAD_CACHE);
     // an abandoned piece: every copy lands before the CTA leaves
-    if (*err)
+    if (*err) {
+      for (; scaled < issued; ++scaled)
+        if (lane == 0) mbar_arrive(bar_full + scaled % C::kStages * 8);
       for (int s = 0; s < C::kStages && s < issued; ++s)
         mbar_wait_drain(bar_full + s * 8, (uint32_t)(((issued - 1 - s) / C::kStages) & 1));
+    }
   } else {
     // ---------------------------------------------------------------- consumers
     const int g4 = lane >> 2, tq = lane & 3;

@@ -201,6 +201,10 @@ __global__ void __launch_bounds__(kWThreads, 2)
   volatile int* const flag = reinterpret_cast<volatile int*>(gbase + C::kOffFlag);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 32) {
+    prefetch_map(&m.q);
+    prefetch_map(&m.k);
+  }
   if (threadIdx.x == 0) {
     mbar_init(bar_a, 1);
     for (int s = 0; s < stages; ++s) {
