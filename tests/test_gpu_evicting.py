@@ -84,12 +84,15 @@ SUM_CASES = [
 ]
 
 
+# prompts of very different lengths
+SUM_RAGGED = [(4, 2, 64, [0, 1500, 3, 0, 90, 64, 1, 200, 0], 0), (8, 2, 128, [5] * 40 + [900] + [130, 1] * 9, 0),
+              (8, 2, 128, [1] * 33 + [1200, 0, 700], 64), (2, 1, 64, [10, 0, 2000], 300)]
 # many heads to a KV head: a query tile of few tokens
 SUM_GROUPS = [(32, 1, 64, [77, 3], 2), (64, 2, 128, [40], 1), (128, 1, 64, [9, 200], 1), (96, 1, 128, [70], 3), (24, 1, 64, [130], 9)]
 
 
 @pytest.mark.parametrize("given", [False, True])
-@pytest.mark.parametrize("hq,hkv,d,lens,window", SUM_CASES + SUM_GROUPS, ids=str)
+@pytest.mark.parametrize("hq,hkv,d,lens,window", SUM_CASES + SUM_GROUPS + SUM_RAGGED, ids=str)
 def test_weight_sums(hq, hkv, d, lens, window, given):
     gen = _rng(len(lens) + 7 * window + d)
     cu = _cu(lens)

@@ -189,6 +189,8 @@ struct WeightParams {
   int32_t* status;
   int pack;              // log2 of the heads that share a query tile
   int stages;            // tile ring (set by the launch)
+  int ragged;            // the grid has only the tiles that the sequences have
+  int lse_tiles, sum_tiles;  // most 128-row tiles of a sequence, as queries and as keys
   // work units of the two passes (grid sizes), and their 128 x 128 tiles: all, of the longest
   long long lse_units, lse_steps, lse_longest;
   long long sum_units, sum_steps, sum_longest;

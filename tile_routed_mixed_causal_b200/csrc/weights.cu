@@ -131,11 +131,48 @@ struct WUnit {
   int ncol, c0;      // column tiles per head, the first of them
   int steps;         // tiles of the stream (all CTAs of the cluster)
 
+  // 128-row tiles of sequence i
+  __device__ static __forceinline__ int tiles(const WeightParams& p, int i) {
+    const int len = __ldg(p.cu + i + 1) - __ldg(p.cu + i);
+    if (!LSE) return (len + kRows - 1) / kRows;
+    const int W = p.n_queries > 0 ? min(len, p.n_queries) : len, qtok = kRows >> p.pack;
+    return (W + qtok - 1) / qtok;
+  }
+
+  // Whole-warp call.  Units: tile t of every sequence before tile t + 1 of any, heads fastest.
   __device__ __forceinline__ void init(const WeightParams& p, long long id) {
     const int H = LSE ? p.Hq >> p.pack : p.Hkv;
     head = (int)(id % H);
     b = (int)((id / H) % p.B);
-    const int t = (int)(id / ((long long)H * p.B));
+    int t = (int)(id / ((long long)H * p.B));
+    if (p.ragged) {
+      // very different lengths: only the tiles there are.  Tiles before t: the sum of min(tiles, t);
+      // t is the largest with no more of them than this unit's index
+      const int lane = threadIdx.x & 31;
+      const int q = (int)(id / H);
+      auto before = [&](int tt) {
+        int n = 0;
+        for (int i = lane; i < p.B; i += 32) n += min(tiles(p, i), tt);
+        return __reduce_add_sync(0xffffffffu, n);
+      };
+      int lo = 0, hi = LSE ? p.lse_tiles : p.sum_tiles;  // before(lo) <= q < before(hi)
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (before(mid) <= q) lo = mid;
+        else hi = mid;
+      }
+      t = lo;
+      int r = q - before(t);  // the r-th sequence that has a tile t
+      for (int i0 = 0; i0 < p.B; i0 += 32) {
+        const uint32_t has = __ballot_sync(0xffffffffu, i0 + lane < p.B && tiles(p, i0 + lane) > t);
+        const int n = __popc(has);
+        if (r < n) {
+          b = i0 + (int)__fns(has, 0, r + 1);
+          break;
+        }
+        r -= n;
+      }
+    }
     seq0 = __ldg(p.cu + b);
     T = __ldg(p.cu + b + 1) - seq0;
     const int W = p.n_queries > 0 ? min(T, p.n_queries) : T;
