@@ -182,3 +182,9 @@ def test_cache_arrays_are_checked(lib):
 def test_plan_sizes(keep, limit):
     with pytest.raises(ValueError):
         api.EvictingDecodePlan(_shape(), keep, limit, device="cpu")
+
+
+def test_plan_needs_a_prompt_first(lib):
+    plan = api.EvictingDecodePlan(_shape(), 2, 4, device="cpu")
+    with pytest.raises(RuntimeError, match="prefill"):
+        plan.step(None, None, None, None)

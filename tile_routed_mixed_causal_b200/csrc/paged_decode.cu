@@ -29,6 +29,8 @@
 // row of 2K tokens: 14 us.
 #include <cuda_fp16.h>
 
+#include <algorithm>
+
 #include "launch_ex.cuh"
 #include "paged_device.cuh"
 
@@ -567,7 +569,7 @@ __global__ void __launch_bounds__(kStepThreads, 2)
 
 // One CTA per (chunk of tokens, KV head, sequence).
 template <int D, int GS>
-__global__ void __launch_bounds__(kFinThreads, 8) paged_finish_kernel(const PagedStepParams p, int chunk) {
+__global__ void __launch_bounds__(kFinThreads, 8) paged_finish_kernel(const PagedStepParams p) {
   __shared__ float s_w[GS * kPieces];  // pieces' m, then their weights 2^(m - M) / L
   __shared__ float s_m[GS], s_il[GS];
   __shared__ float s_red[kFinThreads / 32 * D];
@@ -579,6 +581,8 @@ __global__ void __launch_bounds__(kFinThreads, 8) paged_finish_kernel(const Page
   const int2 info = p.row_info[row];
   const long long row64 = (long long)row * (c.cap + 1) * kTile;
   const int tok = st.x * kTile + st.y;  // tokens before the step
+  // the row's chunk per CTA: whatever the cache's capacity, its tokens are spread over the grid
+  const int chunk = max(256, ((tok + 1) / (int)gridDim.x / 128 + 1) * 128);
   if (row_items(st, c.cap) == 0) {  // idle, bad or full: the row stays
     const PagedRow kind = paged_row(st, c.cap);
     if (x == 0 && g == 0 && t == 0) {
@@ -724,19 +728,16 @@ cudaError_t launch_step_d(const PagedStepParams& p, const PagedMaps& m, cudaStre
   const int grp = c.Hq / c.Hkv;
   cudaError_t e = grp <= 2 ? launch_step_g<D, 2>(p, m, s) : grp <= 4 ? launch_step_g<D, 4>(p, m, s) : launch_step_g<D, 8>(p, m, s);
   if (e != cudaSuccess) return e;
-  // chunks of 256 tokens at least, and about one wave of CTAs over all rows (eight per SM)
+  // about one wave of CTAs over all rows (eight per SM), chunks of 256 tokens at least
   const long long most = ((long long)c.cap + 1) * kTile, rows = (long long)c.B * c.Hkv;
-  long long per = (rows * most / 1184 + 127) / 128 * 128;
-  if (per < 256) per = 256;
-  if (per > most) per = most;
-  const dim3 grid((unsigned)((most + per - 1) / per), c.Hkv, c.B);
-  const int chunk = (int)per;
+  const long long nx = std::min((1184 + rows - 1) / rows, (most + 255) / 256);
+  const dim3 grid((unsigned)nx, c.Hkv, c.B);
   switch (paged_score_stride(grp)) {
-    case 1: return launch_ex(paged_finish_kernel<D, 1>, grid, kFinThreads, 0, s, 0, true, p, chunk);
-    case 2: return launch_ex(paged_finish_kernel<D, 2>, grid, kFinThreads, 0, s, 0, true, p, chunk);
-    case 4: return launch_ex(paged_finish_kernel<D, 4>, grid, kFinThreads, 0, s, 0, true, p, chunk);
-    case 6: return launch_ex(paged_finish_kernel<D, 6>, grid, kFinThreads, 0, s, 0, true, p, chunk);
-    default: return launch_ex(paged_finish_kernel<D, 8>, grid, kFinThreads, 0, s, 0, true, p, chunk);
+    case 1: return launch_ex(paged_finish_kernel<D, 1>, grid, kFinThreads, 0, s, 0, true, p);
+    case 2: return launch_ex(paged_finish_kernel<D, 2>, grid, kFinThreads, 0, s, 0, true, p);
+    case 4: return launch_ex(paged_finish_kernel<D, 4>, grid, kFinThreads, 0, s, 0, true, p);
+    case 6: return launch_ex(paged_finish_kernel<D, 6>, grid, kFinThreads, 0, s, 0, true, p);
+    default: return launch_ex(paged_finish_kernel<D, 8>, grid, kFinThreads, 0, s, 0, true, p);
   }
 }
 
