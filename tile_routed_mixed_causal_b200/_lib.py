@@ -374,24 +374,29 @@ def hybrid_attention_prefill(shape: Shape, hy: Hybrid, q, k, v, kv: QTiles, k_mi
         _stream(stream)))
 
 
-def _expect(name, t, dtype, shape, device):
-    """t: a contiguous tensor of this dtype, shape and device (TraError otherwise)."""
-    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape or t.device != device \
-            or not t.is_contiguous():
-        raise TraError(1, f"{name} must be a contiguous {dtype} tensor of shape {shape} on {device}")
+def _expect(name, t, dtype, shape, index):
+    """Address of t: a contiguous tensor of this dtype and shape on device number `index` (-1: the
+    host); TraError otherwise."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == index and t.shape == shape \
+            and t.is_contiguous():
+        return t.data_ptr()
+    raise TraError(1, f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on "
+                      f"{f'cuda:{index}' if index >= 0 else 'the host'}")
 
 
 def _launch_device(t):
-    """t's device, which has to be the current one: the kernels start there."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+    """Number of t's device, which has to be the current one: the kernels start there."""
+    index = t.get_device() if isinstance(t, torch.Tensor) else -1
+    if index < 0:
         raise TraError(1, "a tensor on a CUDA device is required")
-    if t.get_device() != torch.cuda.current_device():
+    if index != torch.cuda.current_device():
         raise TraError(1, f"the tensors are on {t.device}, which is not the current device")
-    return t.device
+    return index
 
 
-def _addr(t):
-    return None if t is None else t.data_ptr()
+def _on(shape: Shape, index):
+    if shape.cu_dev is None or shape.cu_dev.get_device() != index:
+        raise TraError(1, f"the shape's cu_seqlens must be on cuda:{index}")
 
 
 def attention_weight_sums(shape: Shape, q, k, weights, lse, *, n_queries: int = 0, softmax_scale,
@@ -401,15 +406,15 @@ def attention_weight_sums(shape: Shape, q, k, weights, lse, *, n_queries: int = 
     window's rows are computed and written.  status: device int32 (default: shape.status)."""
     dev = _launch_device(q)
     n, hq, hkv, d = shape.ntok, shape.Hq, shape.Hkv, shape.d
-    if shape.cu_dev is None or shape.cu_dev.device != dev:
-        raise TraError(1, f"the shape's cu_seqlens must be on {dev}")
-    _expect("q", q, torch.bfloat16, (n, hq, d), dev)
-    _expect("k", k, torch.bfloat16, (n, hkv, d), dev)
-    _expect("weights", weights, torch.float32, (n, hkv), dev)
-    _expect("lse", lse, torch.float32, (hq, n), dev)
-    _check(load().attention_weight_sums(
-        shape.c, _addr(q), _addr(k), int(n_queries), float(softmax_scale), _addr(lse), int(bool(lse_given)),
-        _addr(weights), _addr(shape.status if status is None else status), _stream(stream)))
+    _on(shape, dev)
+    f32 = torch.float32
+    q = _expect("q", q, torch.bfloat16, (n, hq, d), dev)
+    k = _expect("k", k, torch.bfloat16, (n, hkv, d), dev)
+    weights = _expect("weights", weights, f32, (n, hkv), dev)
+    lse = _expect("lse", lse, f32, (hq, n), dev)
+    status = shape.status.data_ptr() if status is None else _expect("status", status, torch.int32, (1,), dev)
+    _check(load().attention_weight_sums(shape.c, q, k, int(n_queries), float(softmax_scale), lse, int(bool(lse_given)),
+                                        weights, status, _stream(stream)))
 
 
 class PagedCache:
@@ -438,8 +443,8 @@ class PagedCache:
         else:
             self.t = {n: tensors[n] for n in self.NAMES}
             for n in self.NAMES:
-                _expect(n, self.t[n], spec[n][1], spec[n][0], self.t["k8"].device)
-        self.n_pool, self.device = n_pool, self.t["k8"].device
+                _expect(n, self.t[n], spec[n][1], spec[n][0], self.t["k8"].get_device())
+        self.n_pool, self.device, self.index = n_pool, self.t["k8"].device, self.t["k8"].get_device()
         self._c = _PagedCache(B, Hq, Hkv, d, cap, n_pool, *[self.t[n].data_ptr() for n in self.NAMES])
         self.c = ctypes.byref(self._c)
         nbytes = int(load().tra_paged_workspace_bytes(self.c))
@@ -457,39 +462,37 @@ class PagedCache:
         if t is None:
             return None
         own = self.t[name]
-        _expect(name + "_out", t, own.dtype, own.shape, self.device)
-        return t.data_ptr()
+        return _expect(name + "_out", t, own.dtype, own.shape, self.index)
 
 
 def paged_cache_fill(cache: PagedCache, shape: Shape, k, v, *, keep: int, recent: int = 0, weights=None,
                      stream=None):
     """The prompts of `shape` into the cache's rows, each cut to the `keep` pages of its last
     `recent` tokens and those of largest weight (float32 [ntok, Hkv]; None: the latest)."""
-    dev = _launch_device(k)
-    n = shape.ntok
-    if cache.device != dev or shape.cu_dev is None or shape.cu_dev.device != dev:
-        raise TraError(1, f"the cache and the shape's cu_seqlens must be on {dev}")
-    _expect("k", k, torch.bfloat16, (n, cache.Hkv, cache.d), dev)
-    _expect("v", v, torch.bfloat16, (n, cache.Hkv, cache.d), dev)
+    dev = _launch_device(cache.t["k8"])
+    _on(shape, dev)
+    rows = (shape.ntok, cache.Hkv, cache.d)
+    k = _expect("k", k, torch.bfloat16, rows, dev)
+    v = _expect("v", v, torch.bfloat16, rows, dev)
     if weights is not None:
-        _expect("weights", weights, torch.float32, (n, cache.Hkv), dev)
-    _check(load().paged_cache_fill(cache.c, shape.c, _addr(k), _addr(v), _addr(weights), int(keep), int(recent),
-                                   *cache._scratch, _stream(stream)))
+        weights = _expect("weights", weights, torch.float32, rows[:2], dev)
+    _check(load().paged_cache_fill(cache.c, shape.c, k, v, weights, int(keep), int(recent), *cache._scratch,
+                                   _stream(stream)))
 
 
 def paged_attention_decode(cache: PagedCache, q, k_new, v_new, out, *, softmax_scale, state_out=None,
                            weight_out=None, stream=None):
     """One token per row: attention over the row, its probabilities added to the weights, and the
     append (include/tra.h).  state_out, weight_out: where those go instead of the cache's own."""
-    dev = _launch_device(q)
-    B, d = cache.B, cache.d
-    _expect("q", q, torch.bfloat16, (B, cache.Hq, d), dev)
-    _expect("k_new", k_new, torch.bfloat16, (B, cache.Hkv, d), dev)
-    _expect("v_new", v_new, torch.bfloat16, (B, cache.Hkv, d), dev)
-    _expect("out", out, torch.bfloat16, (B, cache.Hq, d), cache.device)
-    _check(load().paged_attention_decode(
-        cache.c, q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), float(softmax_scale), out.data_ptr(),
-        cache._out("state", state_out), cache._out("weight", weight_out), *cache._scratch, _stream(stream)))
+    dev = _launch_device(cache.t["k8"])
+    heads, kv, bf16 = (cache.B, cache.Hq, cache.d), (cache.B, cache.Hkv, cache.d), torch.bfloat16
+    q = _expect("q", q, bf16, heads, dev)
+    k_new = _expect("k_new", k_new, bf16, kv, dev)
+    v_new = _expect("v_new", v_new, bf16, kv, dev)
+    out = _expect("out", out, bf16, heads, dev)
+    _check(load().paged_attention_decode(cache.c, q, k_new, v_new, float(softmax_scale), out,
+                                         cache._out("state", state_out), cache._out("weight", weight_out),
+                                         *cache._scratch, _stream(stream)))
 
 
 def paged_cache_evict(cache: PagedCache, *, keep: int, recent: int = 0, state_out=None, table_out=None,
