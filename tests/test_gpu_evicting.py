@@ -624,6 +624,41 @@ def test_pages_past_32_bits():
                 assert torch.equal(near[name], big[name][-n:] if name in ("k8", "v8", "sk", "sv") else big[name]), (call, name)
 
 
+def test_decode_of_millions_of_pages():
+    """64 rows of 70,000 pages (a list of more than 2^22 items), all of them the same four: attention over four
+    pages with multiplicities.  (Reading shared pages is all this step does: no tail is full.)"""
+    B, n, d, scale = 64, 70000, 64, 0.125
+    gen = _rng(11)
+    z = lambda *s, t=torch.float32: torch.zeros(s, device=DEV, dtype=t)  # noqa: E731
+    t = dict(k8=torch.randint(-127, 128, (4, TILE, d), generator=gen, device=DEV, dtype=torch.int8),
+             v8=torch.randint(-127, 128, (4, TILE, d), generator=gen, device=DEV, dtype=torch.int8),
+             sk=torch.rand(4, generator=gen, device=DEV) * 0.02 + 0.005, sv=torch.rand(4, generator=gen, device=DEV) * 0.05,
+             table=(torch.arange(n, device=DEV, dtype=torch.int32) % 4).repeat(B, 1, 1).contiguous(), state=z(B, 4, t=torch.int32),
+             weight=z(B, 1, (n + 1) * TILE), pos=z(B, 1, (n + 1) * TILE, t=torch.int32),
+             k_tail=z(B, 1, TILE, d, t=torch.bfloat16), v_tail=z(B, 1, TILE, d, t=torch.bfloat16))
+    t["state"][:, 0] = n
+    cache = tra.PagedCache(B, 1, 1, d, n, tensors=t)
+    q, kn, vn = _normal(gen, B, 1, d), _normal(gen, B, 1, d), _normal(gen, B, 1, d)
+    out = torch.empty_like(q)
+    tra.paged_attention_decode(cache, q, kn, vn, out, softmax_scale=scale)
+    assert int(cache.status) == 0
+    k = (t["k8"].double() * t["sk"].double()[:, None, None]).view(-1, d)
+    v = (t["v8"].double() * t["sv"].double()[:, None, None]).view(-1, d)
+    s = torch.cat([q[:, 0].double() @ k.T, (q[:, 0].double() * kn[:, 0].double()).sum(1, keepdim=True)], 1) * scale
+    many = torch.cat([torch.full((256,), n / 4, device=DEV, dtype=torch.float64), torch.ones(1, device=DEV, dtype=torch.float64)])
+    p = torch.exp(s - s.amax(1, keepdim=True))
+    p = p / (p * many).sum(1, keepdim=True)
+    o = (p[:, :256] * (n / 4)) @ v + p[:, 256:] * vn[:, 0].double()
+    # the sums: a warp adds 8 terms of each of its pages, a quarter of a piece's, one after another in fp32
+    rel = 8 * (n * B / 296) / 4 * 2.0 ** -24 + 2.0 ** -17
+    mag = (p[:, :256] * (n / 4)) @ v.abs() + p[:, 256:] * vn[:, 0].double().abs()
+    assert bool(((out[:, 0].double() - o).abs() <= 2.0 ** -8 * o.abs() + (2.0 ** -10.9 + 2 * rel) * mag).all())
+    w = cache["weight"][:, 0, :n * TILE + 1].double()
+    assert bool(((w[:, :-1].view(B, n // 4, 256) - p[:, None, :256]).abs() <= 2 * rel * p[:, None, :256]).all())
+    assert bool(((w[:, -1] - p[:, 256]).abs() <= 2 * rel * p[:, 256]).all())
+    assert bool((cache["state"][:, :3] == torch.tensor([n, 1, 1], device=DEV)).all())
+
+
 # ================================================================ states and pages out of range
 @pytest.mark.parametrize("state", [(4, 0), (2, 64), (2, -1)])
 def test_bad_states_are_reported_and_left(state):

@@ -108,45 +108,79 @@ __device__ __forceinline__ int row_items(int4 st, int cap) {
   return st.x + 1;
 }
 
-// The list: rows b-major, KV head within, a row's pages then its tail.  Whole-warp call.
-// Returns the number of items; with `find` also the row state index, KV head and item within
-// the row of list item `at`.
+// The list: rows b-major, KV head within, a row's pages then its tail.  (Whole-warp calls.)
 struct ListPos {
   int b, g, item;
 };
-__device__ __forceinline__ long long list_scan(const int4* state, int B, int Hkv, int cap, long long at, bool find,
-                                               ListPos& pos) {
-  const int lane = threadIdx.x & 31;
-  long long base = 0;
-  for (int b0 = 0; b0 < B; b0 += 32) {
-    const int b = b0 + lane;
-    const int it = b < B ? row_items(state[b], cap) : 0;
-    long long s = (long long)it * Hkv;
-    const long long own = s;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long u = __shfl_up_sync(0xffffffffu, s, o);
-      if (lane >= o) s += u;
-    }
-    const long long lo = base + s - own, hi = base + s;
-    if (find) {
-      const uint32_t hit = __ballot_sync(0xffffffffu, own > 0 && at >= lo && at < hi);
-      if (hit) {
-        const int src = __ffs(hit) - 1;
-        const long long l0 = __shfl_sync(0xffffffffu, lo, src);
-        const int n = __shfl_sync(0xffffffffu, it, src);
-        pos.b = b0 + src;
-        pos.g = (int)((at - l0) / n);
-        pos.item = (int)((at - l0) % n);
-      }
-    }
-    base += __shfl_sync(0xffffffffu, s, 31);
-  }
-  return base;
-}
+// A list of fewer items than this is shared out in 32-bit arithmetic: the 64-bit divisions were a
+// tenth of a short step.
+constexpr long long kShortList = 1ll << 22;
 // pieces in use, and the first item of piece i
 __device__ __forceinline__ int pieces_of(long long items) { return items < kPieces ? (int)items : kPieces; }
-__device__ __forceinline__ long long piece_start(long long items, int pieces, int i) { return items * i / pieces; }
+__device__ __forceinline__ long long piece_start(long long items, int pieces, int i) {
+  if (items < kShortList) return (uint32_t)items * (uint32_t)i / (uint32_t)pieces;
+  return items * i / pieces;
+}
+
+// Items before this lane's sequence b0 + lane (lo) and behind it (hi), `base` before the chunk.
+__device__ __forceinline__ void list_chunk(int items, int Hkv, long long base, long long& lo, long long& hi) {
+  const int lane = threadIdx.x & 31;
+  long long s = (long long)items * Hkv;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long u = __shfl_up_sync(0xffffffffu, s, o);
+    if (lane >= o) s += u;
+  }
+  hi = base + s;
+  lo = hi - (long long)items * Hkv;
+}
+
+// Piece `piece` of the list: its first item and the one behind its last; pos: the sequence,
+// KV head and item within the row of the first.  False: no such piece.
+__device__ __forceinline__ bool list_piece(const int4* state, int B, int Hkv, int cap, int piece, long long& first,
+                                           long long& last, ListPos& pos) {
+  const int lane = threadIdx.x & 31;
+  const int it0 = lane < B ? row_items(state[lane], cap) : 0;  // the first 32 sequences
+  long long lo0, hi0;
+  list_chunk(it0, Hkv, 0, lo0, hi0);
+  const long long base1 = __shfl_sync(0xffffffffu, hi0, 31);
+  long long items = base1;
+  for (int b0 = 32; b0 < B; b0 += 32) {
+    const long long n = b0 + lane < B ? (long long)row_items(state[b0 + lane], cap) * Hkv : 0;
+    long long s = n;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    items += s;
+  }
+  const int pieces = pieces_of(items);
+  if (piece >= pieces) return false;
+  first = piece_start(items, pieces, piece);
+  last = piece_start(items, pieces, piece + 1);
+  int it = it0, b0 = 0;
+  long long lo = lo0, hi = hi0;
+  while (true) {  // the chunk of sequences that holds it (there is one)
+    const uint32_t hit = __ballot_sync(0xffffffffu, hi > lo && first >= lo && first < hi);
+    if (hit) {
+      const int src = __ffs(hit) - 1;
+      const long long at = first - __shfl_sync(0xffffffffu, lo, src);
+      const int n = __shfl_sync(0xffffffffu, it, src);
+      pos.b = b0 + src;
+      if (items < kShortList) {
+        pos.g = (int)((uint32_t)at / (uint32_t)n);
+        pos.item = (int)((uint32_t)at % (uint32_t)n);
+      } else {
+        pos.g = (int)(at / n);
+        pos.item = (int)(at % n);
+      }
+      return true;
+    }
+    const long long base = __shfl_sync(0xffffffffu, hi, 31);
+    b0 += 32;
+    if (b0 >= B) return false;
+    it = b0 + lane < B ? row_items(state[b0 + lane], cap) : 0;
+    list_chunk(it, Hkv, base, lo, hi);
+  }
+}
 
 template <int D, int GRP>
 struct StepCfg {
@@ -199,11 +233,8 @@ __global__ void __launch_bounds__(kStepThreads, 2)
   if (blockIdx.x == 0)
     for (int b = t; b < c.B; b += kStepThreads) p.ws_state[b] = state[b];
   ListPos pos{0, 0, 0};
-  const long long items = list_scan(state, c.B, c.Hkv, c.cap, 0, false, pos);
-  const int pieces = pieces_of(items);
-  if ((int)blockIdx.x >= pieces) return;  // uniform
-  const long long lo = piece_start(items, pieces, blockIdx.x), hi = piece_start(items, pieces, blockIdx.x + 1);
-  list_scan(state, c.B, c.Hkv, c.cap, lo, true, pos);
+  long long lo = 0, hi = 0;
+  if (!list_piece(state, c.B, c.Hkv, c.cap, blockIdx.x, lo, hi, pos)) return;  // uniform
   __syncthreads();
 
   // the piece row by row: row state st, items [i0, i1) of it, the row's last item its tail
