@@ -450,6 +450,9 @@ STEPS = [
     (7, 1, 128, 6, [(5, 63), (-1, 0), (6, 62), (3, 0)]), (8, 8, 64, 5, [(4, 30), (5, 63), (2, 15), (-7, 9)]),
     (12, 4, 64, 40, [(37, 16), (1, 31), (39, 48)]), (16, 2, 128, 33, [(33, 3), (20, 63)]), (2, 2, 128, 70, [(64, 1)]),
     (6, 2, 128, 12, [(11, 47), (0, 63), (5, 32), (2, 33)] * 3), (8, 8, 128, 130, [(128, 40), (70, 63)]),
+    # room for many pages: a warp takes whole pages
+    (32, 8, 128, 300, [(8, 17)]), (14, 2, 64, 600, [(37, 16), (20, 63)]), (8, 8, 128, 400, [(128, 40), (70, 63)]),
+    (7, 1, 128, 1300, [(300, 62), (-1, 0), (5, 63)]), (2, 1, 64, 1300, [(900, 5), (0, 0)]),
 ]
 
 
@@ -507,11 +510,12 @@ def test_decode_ranges(q_scale, v_scale):
     ref.same()
 
 
-def test_decode_of_many_rows():
+@pytest.mark.parametrize("cap", [5, 20])
+def test_decode_of_many_rows(cap):
     """More rows than CTAs, and than a warp scans at a time."""
     rows = [((3 * i) % 4, (7 * i) % 64) for i in range(75)]
     rows[40] = (-1, 0)
-    cache, (q, kn, vn) = _filled(rows, 8, 4, 64, 5, seed=3)
+    cache, (q, kn, vn) = _filled(rows, 8, 4, 64, cap, seed=3)
     ref = Mirror(cache)
     out = torch.empty_like(q)
     tra.paged_attention_decode(cache, q, kn, vn, out, softmax_scale=0.125)

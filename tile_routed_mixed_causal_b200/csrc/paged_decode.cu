@@ -7,8 +7,8 @@
 // ragged rows and single long ones load every SM alike.  A CTA is a producer warp and four
 // consumer warps.  The producer streams pages (8 KB of K codes, 8 KB of V codes at d = 128,
 // TMA with the swizzle that makes the reads below bank-conflict free) through a ring; each
-// consumer warp takes every fourth page with its own softmax state for all query heads of
-// the group, so every cached byte is read once:
+// consumer warp takes every fourth page (a quarter of every page, where there are few) with its
+// own softmax state for all query heads of the group, so every cached byte is read once:
 //   S = K q:    mma m16n8k16, M = 16 keys, N = 8 heads.  K codes become f16 exactly; q is
 //               scaled per head by a power of two so that its bf16 values are f16 exactly
 //               (all within 2^31 of the head's largest), products are exact and summed in fp32:
@@ -30,6 +30,7 @@
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "launch_ex.cuh"
 #include "paged_device.cuh"
@@ -41,6 +42,7 @@ constexpr int kCons = 4;                       // consumer warps
 constexpr int kStepThreads = 32 * (kCons + 1);
 constexpr int kPieces = 296;                   // CTAs of the list: two per SM
 constexpr int kFinThreads = 128;
+constexpr int kSplitItems = 8;                 // items of a piece up to which its pages are split
 constexpr float kSlack = 8.0f;                 // log2 units p may pass 1 before a rescale
 
 __device__ __forceinline__ float ex2(float x) {
@@ -199,7 +201,9 @@ struct StepCfg {
   static constexpr int kSmem = kOffMisc + 64 + 1024;
 };
 
-template <int D, int GRP>
+// SPLIT: the warps share every page, 16 keys each (pieces are short: a page's own latency is what the
+// step waits for).
+template <int D, int GRP, bool SPLIT>
 __global__ void __launch_bounds__(kStepThreads, 2)
     paged_step_kernel(const __grid_constant__ PagedStepParams p, const __grid_constant__ PagedMaps m) {
   using C = StepCfg<D, GRP>;
@@ -224,7 +228,7 @@ __global__ void __launch_bounds__(kStepThreads, 2)
   if (t == 0) {
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(bar_full + s * 8, 2);  // the copies' bytes, and the scales
-      mbar_init(bar_empty + s * 8, 1);
+      mbar_init(bar_empty + s * 8, SPLIT ? kCons : 1);
     }
     *err = 0;
     fence_barrier_init();
@@ -319,7 +323,7 @@ __global__ void __launch_bounds__(kStepThreads, 2)
     const int g4 = lane >> 2, tq = lane & 3;
     const int mrow = (lane & 7) + 8 * ((lane >> 3) & 1), mch = lane >> 4;  // ldmatrix row, chunk
     const int gs = paged_score_stride(grp);
-    int next = warp;  // this warp's next page in the piece's stream of pages
+    int next = SPLIT ? 0 : warp;  // this warp's next page in the piece's stream of pages
     int seen = 0;     // pages of the rows before
     bool ok = true;   // once a wait has run out: no more pages, but every barrier
     for_rows([&](int b, int g, int4 st, int i0, int i1) -> bool {
@@ -391,30 +395,23 @@ __global__ void __launch_bounds__(kStepThreads, 2)
         }
       };
 
-      for (; ok && next < seen + npage; next += kCons) {
-        const int s = next % C::kStages;
-        const int item = i0 + next - seen;
-        // Stage s last held page next - kStages, another warp's: its release (which this
-        // fill waited for) makes the full barrier's phase before this one known to be
-        // complete, so the parity wait on it is exact.
-        ok = (next < C::kStages || mbar_wait(bar_empty + s * 8, ((next / C::kStages) - 1) & 1, err)) &&
-             mbar_wait(bar_full + s * 8, (next / C::kStages) & 1, err);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
+      // NB blocks of 16 keys from block k0 of the page in stage s
+      auto attend = [&](auto blocks, int k0, int s, int item) {
+        constexpr int NB = decltype(blocks)::value;
         const uint32_t kb = base + s * C::kStageBytes, vb = kb + C::kTileBytes;
         const float2 sc = scale[s];
-        float sr[4][4];
+        float sr[NB][4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
+        for (int k = 0; k < NB; ++k)
 #pragma unroll
           for (int x = 0; x < 4; ++x) sr[k][x] = 0.0f;
 #pragma unroll
         for (int cb = 0; cb < D / 32; ++cb) {
           const uint32_t off = swz<D>(mrow, 2 * cb + mch);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
+          for (int k = 0; k < NB; ++k) {
             uint32_t r[4];  // keys 16k + g4, + 8; channels 32 cb + 4 tq .., + 16
-            ldsm4(kb + 16 * D * k + off, r);
+            ldsm4(kb + 16 * D * (k0 + k) + off, r);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               const uint32_t u0 = r[2 * h] ^ 0x80808080u, u1 = r[2 * h + 1] ^ 0x80808080u;
@@ -426,24 +423,24 @@ __global__ void __launch_bounds__(kStepThreads, 2)
         const float f0 = sc.x * hs[0], f1 = sc.x * hs[1];
         float mt[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
+        for (int k = 0; k < NB; ++k) {
           sr[k][0] *= f0;
           sr[k][1] *= f1;
           sr[k][2] *= f0;
           sr[k][3] *= f1;
           mt[0] = fmaxf(mt[0], fmaxf(sr[k][0], sr[k][2]));
           mt[1] = fmaxf(mt[1], fmaxf(sr[k][1], sr[k][3]));
-          store_score(item * kTile + 16 * k + g4, sr[k][0], sr[k][1]);
-          store_score(item * kTile + 16 * k + g4 + 8, sr[k][2], sr[k][3]);
+          store_score(item * kTile + 16 * (k0 + k) + g4, sr[k][0], sr[k][1]);
+          store_score(item * kTile + 16 * (k0 + k) + g4 + 8, sr[k][2], sr[k][3]);
         }
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
           for (int x = 4; x < 32; x <<= 1) mt[h] = fmaxf(mt[h], __shfl_xor_sync(0xffffffffu, mt[h], x));
         raise(mt);
-        uint32_t pb[4][2];
+        uint32_t pb[NB][2];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
+        for (int k = 0; k < NB; ++k) {
           const float p0 = ex2(sr[k][0] - mr[0]), p1 = ex2(sr[k][1] - mr[1]);
           const float p2 = ex2(sr[k][2] - mr[0]), p3 = ex2(sr[k][3] - mr[1]);
           lr[0] += p0 + p2;
@@ -458,9 +455,9 @@ __global__ void __launch_bounds__(kStepThreads, 2)
 #pragma unroll
           for (int x = 0; x < 4; ++x) acc[0][x] = acc[1][x] = 0.0f;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
+          for (int k = 0; k < NB; ++k) {
             uint32_t r[4];  // channels 32 cb + 16 h + 2 g4, + 1 of keys 16k + 2 tq, + 1 (, + 8)
-            ldsm4t(vb + 16 * D * k + off, r);
+            ldsm4t(vb + 16 * D * (k0 + k) + off, r);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               const uint32_t u0 = r[2 * h] ^ 0x80808080u, u1 = r[2 * h + 1] ^ 0x80808080u;
@@ -473,6 +470,18 @@ __global__ void __launch_bounds__(kStepThreads, 2)
 #pragma unroll
             for (int x = 0; x < 4; ++x) o[2 * cb + h][x] = fmaf(acc[h][x], sc.y, o[2 * cb + h][x]);
         }
+      };
+      for (; ok && next < seen + npage; next += SPLIT ? 1 : kCons) {
+        const int s = next % C::kStages;
+        const int item = i0 + next - seen;
+        // Stage s last held page next - kStages.  Where that was another warp's, its release (which
+        // this fill waited for) makes the full barrier's phase before this one known to be
+        // complete, so the parity wait on it is exact.
+        ok = (SPLIT || next < C::kStages || mbar_wait(bar_empty + s * 8, ((next / C::kStages) - 1) & 1, err)) &&
+             mbar_wait(bar_full + s * 8, (next / C::kStages) & 1, err);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        attend(std::integral_constant<int, SPLIT ? 1 : 4>{}, SPLIT ? warp : 0, s, item);
         __syncwarp();
         if (lane == 0) mbar_arrive(bar_empty + s * 8);
       }
@@ -744,13 +753,21 @@ __global__ void __launch_bounds__(kFinThreads, 8) paged_finish_kernel(const Page
         make_int4(st.x + (st.y == kTile - 1), (st.y + 1) % kTile, st.z + 1, st.w);
 }
 
-template <int D, int GRP>
-cudaError_t launch_step_g(const PagedStepParams& p, const PagedMaps& m, cudaStream_t s) {
+template <int D, int GRP, bool SPLIT>
+cudaError_t launch_step_s(const PagedStepParams& p, const PagedMaps& m, cudaStream_t s) {
   using C = StepCfg<D, GRP>;
   static SmemLimit limit;
-  cudaError_t e = limit.raise(paged_step_kernel<D, GRP>, C::kSmem);
+  cudaError_t e = limit.raise(paged_step_kernel<D, GRP, SPLIT>, C::kSmem);
   if (e != cudaSuccess) return e;
-  return launch_ex(paged_step_kernel<D, GRP>, dim3(kPieces), kStepThreads, C::kSmem, s, 0, false, p, m);
+  return launch_ex(paged_step_kernel<D, GRP, SPLIT>, dim3(kPieces), kStepThreads, C::kSmem, s, 0, false, p, m);
+}
+
+template <int D, int GRP>
+cudaError_t launch_step_g(const PagedStepParams& p, const PagedMaps& m, cudaStream_t s) {
+  // Where the cache has room for few pages per piece the warps split them (a row of 2K tokens: 11.0
+  // -> 9.6 us; 27 pages per piece split or not by a branch in one kernel: 3 % slower than apart).
+  const long long most = (long long)p.c.B * p.c.Hkv * (p.c.cap + 1);
+  return most <= (long long)kSplitItems * kPieces ? launch_step_s<D, GRP, true>(p, m, s) : launch_step_s<D, GRP, false>(p, m, s);
 }
 
 template <int D>
