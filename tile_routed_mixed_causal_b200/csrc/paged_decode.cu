@@ -26,7 +26,7 @@
 // the output and the new state, and quantises a tail that became full.  The split is what
 // bounds the step: 2 d bytes of codes per cached token, against 4 grp + 8 bytes here.
 // Batch 16 x 32K, 32/8 heads, d 128: split 178 us (6.2 TB/s, 94 % of a copy), step 207 us; a single
-// row of 2K tokens: 14 us.
+// row of 2K tokens: 9.3 us.
 #include <cuda_fp16.h>
 
 #include <algorithm>
