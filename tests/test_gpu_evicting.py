@@ -765,6 +765,38 @@ def test_captured_steps():
             assert torch.equal(a[n], b[n]), n
 
 
+def test_captured_prompt():
+    """Weight sums and a fill from them, captured and replayed on other inputs."""
+    lens = [300, 64, 777]
+    cu, gen = _cu(lens), _rng(4)
+    shape, n = tra.Shape(cu, 8, 2, 128), sum(lens)
+    q, k, v = (_normal(gen, n, h, 128) for h in (8, 2, 2))
+    made = []
+    for _ in range(2):
+        cache, _ = _filled([(-1, 0)] * 3, 8, 2, 128, 6, seed=1)
+        made.append((cache, torch.zeros(n, 2, device=DEV), torch.zeros(8, n, device=DEV)))
+
+    def work(cache, w, lse):
+        tra.attention_weight_sums(shape, q, k, w, lse, n_queries=64, softmax_scale=0.09)
+        tra.paged_cache_fill(cache, shape, k, v, keep=4, recent=20, weights=w)
+
+    work(*made[1])
+    torch.cuda.synchronize()
+    s, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        work(*made[0])
+    for i in range(3):
+        q.copy_(_normal(_rng(i), *q.shape))
+        v.copy_(_normal(_rng(10 + i), *v.shape))
+        g.replay()
+        torch.cuda.synchronize()
+        work(*made[1])
+        for a, b in zip(made[0][1:], made[1][1:]):
+            assert torch.equal(a, b)
+        for name in made[0][0].NAMES:
+            assert torch.equal(made[0][0][name], made[1][0][name]), name
+
+
 def test_streams():
     """Two caches stepped on two streams at once, and weight sums on a stream of its own."""
     made = [_filled([(60, 20), (33, 63)], 8, 8, 128, 64, seed=s) for s in (1, 2)]
