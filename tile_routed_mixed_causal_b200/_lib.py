@@ -453,6 +453,9 @@ class PagedCache:
         self.workspace = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
         self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
         self._scratch = (self.workspace.data_ptr(), nbytes, self.status.data_ptr())
+        # what was set above is there for a first call on any stream
+        if self.index >= 0 and not torch.cuda.is_current_stream_capturing():
+            torch.cuda.current_stream(self.device).synchronize()
 
     def __getitem__(self, k):
         return self.t[k]

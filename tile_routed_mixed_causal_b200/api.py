@@ -17,6 +17,7 @@ every step leaves them at zero).
 """
 from __future__ import annotations
 
+import contextlib
 import math
 
 import torch
@@ -141,17 +142,31 @@ class HybridPrefillPlan:
         self.attend(q, k, v, out, lse, scale, stream)
 
 
+def _made_on(stream, device):
+    """Context whose new tensors belong to the stream that a call is given (None: the current
+    one): their memory is neither taken from work still queued on another stream nor handed to
+    one before the call's kernels are done."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = int(stream)
+        stream = torch.cuda.ExternalStream(handle, device) if handle else torch.cuda.default_stream(device)
+    return torch.cuda.stream(stream)
+
+
 def prompt_importance(shape: L.Shape, q, k, n_queries: int = 64, lse=None, scale=None, stream=None):
     """Accumulated attention weight of the prompt's keys, float32 [ntok, Hkv]: the importance
     that hybrid_select_tokens and paged_cache_fill take.  n_queries: the last queries of each
-    sequence that count (0: all); lse: what a prefill wrote, or None to compute it."""
+    sequence that count (0: all); lse: what a prefill wrote, or None to compute it.  The result
+    is made on `stream`, as if that were the current one."""
     scale = 1.0 / math.sqrt(shape.d) if scale is None else scale
-    weights = torch.empty((shape.ntok, shape.Hkv), dtype=torch.float32, device=q.device)
     given = lse is not None
-    if not given:
-        lse = torch.empty((shape.Hq, shape.ntok), dtype=torch.float32, device=q.device)
-    L.attention_weight_sums(shape, q, k, weights, lse, n_queries=n_queries, softmax_scale=scale,
-                            lse_given=given, stream=stream)
+    with _made_on(stream, q.device):
+        weights = torch.empty((shape.ntok, shape.Hkv), dtype=torch.float32, device=q.device)
+        if not given:
+            lse = torch.empty((shape.Hq, shape.ntok), dtype=torch.float32, device=q.device)
+        L.attention_weight_sums(shape, q, k, weights, lse, n_queries=n_queries, softmax_scale=scale,
+                                lse_given=given, stream=stream)
     return weights
 
 
@@ -175,7 +190,8 @@ class EvictingDecodePlan:
         return self.cache.status
 
     def prefill(self, q, k, v, lse=None, scale=None, stream=None):
-        """Weigh the prompt's keys (by the last n_queries queries) and store what stays."""
+        """Weigh the prompt's keys (by the last n_queries queries) and store what stays; the weights,
+        made on `stream`."""
         w = prompt_importance(self.shape, q, k, self.n_queries, lse, scale, stream)
         L.paged_cache_fill(self.cache, self.shape, k, v, keep=self.keep, recent=self.recent, weights=w,
                            stream=stream)
