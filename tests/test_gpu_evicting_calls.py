@@ -63,3 +63,25 @@ def test_plan_on_a_stream():
     for n in plans[0].cache.NAMES:
         assert torch.equal(plans[0].cache[n], plans[1].cache[n]), n
     assert int(plans[1].status) == 0
+
+
+# ================================================================ the status word of a shape
+def test_first_call_in_a_capture():
+    """The first call on a shape is a captured one: a replay adds to the shape's status word and clears
+    nothing that an earlier call has left there."""
+    hq, hkv, d, n = 4, 2, 64, 200
+    gen = _rng(31)
+    q, k = _normal(gen, n, hq, d), _normal(gen, n, hkv, d)
+    w, lse = torch.zeros(n, hkv, device=DEV), torch.zeros(hq, n, device=DEV)
+    tra.attention_weight_sums(tra.Shape([0, n], hq, hkv, d), q, k, w, lse, softmax_scale=0.125)     # loads the kernels
+    want = w.clone()
+    shape = tra.Shape([0, n], hq, hkv, d)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=torch.cuda.Stream()):
+        tra.attention_weight_sums(shape, q, k, w, lse, softmax_scale=0.125)
+    shape.status.fill_(tra.DEV_TIMEOUT)
+    w.zero_()
+    g.replay()
+    torch.cuda.synchronize()
+    assert int(shape.status) == tra.DEV_TIMEOUT and torch.equal(w, want)

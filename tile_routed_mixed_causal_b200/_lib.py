@@ -156,10 +156,12 @@ class Shape:
 
     def __init__(self, cu_seqlens, Hq: int, Hkv: int, d: int, device="cuda"):
         self.cu_host = np.ascontiguousarray(np.asarray(cu_seqlens, np.int32))
-        self.cu_dev = torch.as_tensor(self.cu_host).to(device) if device is not None else None
+        self.cu_dev = self._status = None
+        if device is not None:  # cu_seqlens and, behind them, the status word: one copy, done on return
+            words = torch.as_tensor(np.append(self.cu_host, np.int32(0))).to(device)
+            self.cu_dev, self._status = words[:-1], words[-1:]
         self.B = len(self.cu_host) - 1
         self.Hq, self.Hkv, self.d = Hq, Hkv, d
-        self._status = None
         self._c = _Shape(self.B, Hq, Hkv, d,
                          self.cu_dev.data_ptr() if self.cu_dev is not None else 16,
                          self.cu_host.ctypes.data)
@@ -170,9 +172,8 @@ class Shape:
 
     @property
     def status(self):
-        """Device status word (TRA_DEV_* bits) of the calls on this shape that are given none."""
-        if self._status is None:
-            self._status = torch.zeros(1, dtype=torch.int32, device=self.cu_dev.device)
+        """Device status word (TRA_DEV_* bits) of the calls on this shape that are given none; None for a
+        shape without a device."""
         return self._status
 
     @property
