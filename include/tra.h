@@ -462,13 +462,13 @@ TRA_API tra_status attention_weight_sums(const tra_shape* shape, const uint16_t*
 
 /* device status word bits of the evicting cache */
 #define TRA_DEV_CACHE_FULL 0x8   /* a row has no free page for a step's full tail or an eviction's pages */
-#define TRA_DEV_BAD_CACHE 0x10   /* a page number or a row state out of range */
+#define TRA_DEV_BAD_CACHE 0x10   /* a page number or a row state out of range: see the calls */
 
 /*
  * The cache: B rows of Hkv heads.  A row holds n_pages pages of 64 tokens per head and a
  * bf16 tail of 0 to 63 tokens, in order; state[b] = {n_pages, tail_len, seen, 0}, where
  * `seen` counts every token the row was ever given.  A row with n_pages < 0 is idle:
- * every call leaves it as it is.  table[b][g][i] is the page of head g's tokens
+ * every call but a fill leaves it as it is.  table[b][g][i] is the page of head g's tokens
  * 64 i .. 64 i + 63; its entries from n_pages on are the row's free pages.  All cap
  * entries must be different numbers in [0, n_pool), over all rows and heads.
  * A page is 64 x d codes (two's complement, row = token) of K and of V, each with one
@@ -476,6 +476,9 @@ TRA_API tra_status attention_weight_sums(const tra_shape* shape, const uint16_t*
  * (position in the sequence) are per token in the row's order, the tail behind the pages;
  * entries behind the last token mean nothing and are left as they were.
  * All device memory, caller-owned, 16-byte aligned.
+ * A row whose state is out of range, or one of whose page numbers that a fill or an eviction
+ * would read or write by is, sets TRA_DEV_BAD_CACHE and stays as it is, in all its heads; what
+ * a step does then is said there.  Other rows go on.
  */
 typedef struct {
   int32_t B, Hq, Hkv, d;    /* Hq / Hkv <= 8; d 64 or 128 */
@@ -527,7 +530,10 @@ TRA_API tra_status paged_cache_fill(const tra_paged_cache* cache, const tra_shap
  * tokens.  state_out and weight_out are the cache's own arrays or do not overlap them.
  * A row whose tail would fill with no free page left sets TRA_DEV_CACHE_FULL, keeps its
  * state and weights (state_out and weight_out receive them as they are) and leaves its
- * output and tail untouched.
+ * output and tail untouched.  A row with a page number out of range (of its pages, or of a
+ * full tail's page) sets TRA_DEV_BAD_CACHE and keeps its state, so that it loses no token;
+ * the heads with such a number leave their output and weights as they were, the others
+ * have given theirs.
  */
 TRA_API tra_status paged_attention_decode(const tra_paged_cache* cache, const uint16_t* q,
                                           const uint16_t* k_new, const uint16_t* v_new,

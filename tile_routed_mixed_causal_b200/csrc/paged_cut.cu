@@ -1,7 +1,8 @@
 // paged_cut.cu -- filling the evicting cache from a prompt and shrinking it: both choose a
 // row's survivors by accumulated weight and write them as pages of 64 quantised tokens.
 //
-// Selection, one CTA of 1024 threads per (sequence, KV head): the weights' ordered bits are
+// Selection, one CTA of 1024 threads per (sequence, KV head), and one per sequence that checks its
+// page numbers: the weights' ordered bits are
 // staged once in shared memory, protected tokens as the largest; a radix select (three digits
 // of 11, 11 and 10 bits) finds the last key that survives, and one ascending pass writes the
 // survivors' indices at their ranks, ties taken in order.  Bound by latency: a dozen
@@ -66,6 +67,51 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* tmp, uint32
   return tmp[warp] + s - v;
 }
 
+// Evict: the row is to be cut, and has the free pages for it.
+__device__ __forceinline__ bool cut_fits(const PagedCutParams& p, int4 st) {
+  return paged_row(st, p.c.cap) == kRowOk && st.x > p.keep && st.x <= p.c.cap - p.keep;
+}
+
+// What becomes of row b, for the kernels behind the selection: the CTA beside those of its heads.
+// Where one of the page numbers that the row's pages would be read by and written to is out of
+// range, in any head, the whole row stays.  (Checked by the selections themselves, and joined by
+// the pages' CTAs, it cost each of the two kernels half a microsecond.)
+template <bool FILL>
+__device__ __forceinline__ void check_row(const PagedCutParams& p, int b) {
+  const tra_paged_cache& c = p.c;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int4 st;      // as paged_write_kernel takes it
+  int used;     // table entries of each head
+  if (FILL) {
+    const int total = __ldg(p.cu + b + 1) - __ldg(p.cu + b);
+    used = min(total / kTile, p.keep);
+    st = make_int4(used, total % kTile, total, 1);
+  } else {
+    const int4 s = reinterpret_cast<const int4*>(c.state)[b];
+    const PagedRow kind = paged_row(s, c.cap);
+    const bool cut = cut_fits(p, s);
+    st = make_int4(s.x, s.y, kind == kRowOk, cut);
+    used = cut ? s.x + p.keep : 0;
+    if (threadIdx.x == 0) {
+      if (kind == kRowBad) atomicOr(p.status, TRA_DEV_BAD_CACHE);
+      if (kind == kRowOk && s.x > p.keep && !cut) atomicOr(p.status, TRA_DEV_CACHE_FULL);
+    }
+  }
+  bool bad = false;
+  const int parts = max(1, kSelThreads / 32 / c.Hkv);  // warps of a head
+  for (int u = warp; u < c.Hkv * parts; u += kSelThreads / 32) {
+    const int32_t* const table = c.table + ((long long)b * c.Hkv + u / parts) * c.cap;
+#pragma unroll 4
+    for (int k = u % parts * 32 + lane; k < used; k += 32 * parts) bad |= table[k] < 0 || table[k] >= c.n_pool;
+  }
+  bad = __syncthreads_or(bad);
+  if (threadIdx.x == 0) {
+    if (bad) atomicOr(p.status, TRA_DEV_BAD_CACHE);
+    st.w = st.w && !bad;
+    p.ws_state[b] = st;
+  }
+}
+
 template <bool FILL>
 __global__ void __launch_bounds__(kSelThreads) paged_select_kernel(const PagedCutParams p, int stage) {
   extern __shared__ __align__(16) uint32_t keys[];
@@ -76,6 +122,10 @@ __global__ void __launch_bounds__(kSelThreads) paged_select_kernel(const PagedCu
   grid_release();
   const int g = blockIdx.x, b = blockIdx.y, t = threadIdx.x, warp = t >> 5, lane = t & 31;
   const tra_paged_cache& c = p.c;
+  if (g == c.Hkv) {
+    check_row<FILL>(p, b);
+    return;
+  }
   const int row = b * c.Hkv + g;
   const long long row64 = (long long)row * (c.cap + 1) * kTile;
 
@@ -86,18 +136,9 @@ __global__ void __launch_bounds__(kSelThreads) paged_select_kernel(const PagedCu
     total = __ldg(p.cu + b + 1) - from;
     body = total / kTile * kTile;
     n = min(body / kTile, p.keep);
-    if (g == 0 && t == 0) p.ws_state[b] = make_int4(n, total - body, total, 1);
   } else {
     const int4 st = reinterpret_cast<const int4*>(c.state)[b];
-    const PagedRow kind = paged_row(st, c.cap);
-    const bool full = kind == kRowOk && st.x > p.keep && st.x > c.cap - p.keep;
-    const bool cut = kind == kRowOk && st.x > p.keep && !full;
-    if (g == 0 && t == 0) {
-      p.ws_state[b] = make_int4(st.x, st.y, kind == kRowOk, cut);
-      if (kind == kRowBad) atomicOr(p.status, TRA_DEV_BAD_CACHE);
-      if (full) atomicOr(p.status, TRA_DEV_CACHE_FULL);
-    }
-    if (!cut) return;
+    if (!cut_fits(p, st)) return;
     body = st.x * kTile;
     n = p.keep;
     total = body + st.y;
@@ -387,7 +428,7 @@ __global__ void __launch_bounds__(PageCfg<D, FILL>::kThreads, FILL ? 4 : 7)
   const tra_paged_cache& c = p.c;
   grid_release();
   grid_wait();
-  const int4 st = p.ws_state[b];  // fill {pages, tail, seen, 1}, evict {pages before, tail, valid, cut}
+  const int4 st = p.ws_state[b];  // fill {pages, tail, seen, goes}, evict {pages before, tail, valid, cut}
   const int row = b * c.Hkv + g;
   const long long row64 = (long long)row * (c.cap + 1) * kTile;
   const int32_t* const table = c.table + (long long)row * c.cap;
@@ -397,6 +438,7 @@ __global__ void __launch_bounds__(PageCfg<D, FILL>::kThreads, FILL ? 4 : 7)
   if (grp_i == groups) {  // what lies behind the pages
     const int4 old = reinterpret_cast<const int4*>(c.state)[b];
     if (FILL) {  // the tail's rows, weights and positions
+      if (!st.w) return;
       const int from = __ldg(p.cu + b) + st.z - st.y;
       const uint16_t* const x = is_v ? p.v : p.k;
       uint16_t* const tail = is_v ? c.v_tail : c.k_tail;
@@ -441,15 +483,8 @@ __global__ void __launch_bounds__(PageCfg<D, FILL>::kThreads, FILL ? 4 : 7)
     for (int y = 0; y < C::kRowsEach; ++y) src[y] = s[r0 + y * C::kRowStep];
     tok = t < kTile ? s[t] : 0;
     if (!FILL) {  // evict: the rows of the codes
-      bool bad = false;
 #pragma unroll
-      for (int y = 0; y < C::kRowsEach; ++y) {
-        const int page = table[src[y] / kTile];
-        const bool in = page >= 0 && page < c.n_pool;
-        bad |= !in;
-        src[y] = (in ? page * kTile : 0) + src[y] % kTile;
-      }
-      if (bad) atomicOr(p.status, TRA_DEV_BAD_CACHE);
+      for (int y = 0; y < C::kRowsEach; ++y) src[y] = table[src[y] / kTile] * kTile + src[y] % kTile;
     }
   };
   auto fetch = [&](int i, const int (&src)[C::kRowsEach], int tok, PageRows<D, FILL>& x) {
@@ -494,10 +529,6 @@ __global__ void __launch_bounds__(PageCfg<D, FILL>::kThreads, FILL ? 4 : 7)
       }
     }
     am = block_max<NT>(am, r);
-    if (x.page < 0 || x.page >= c.n_pool) {
-      if (t == 0) atomicOr(p.status, TRA_DEV_BAD_CACHE);
-      return;
-    }
     int8_t* const dst = codes + (long long)x.page * kTile * D;
     if constexpr (FILL) {
       const BlockScale bs(am);
@@ -575,7 +606,7 @@ cudaError_t launch_cut(const PagedCutParams& p, cudaStream_t s) {
   static SmemLimit limit;
   cudaError_t e = limit.raise(paged_select_kernel<FILL>, kSpan * 4);
   if (e != cudaSuccess) return e;
-  e = launch_ex(paged_select_kernel<FILL>, dim3(c.Hkv, c.B), kSelThreads, smem, s, 0, false, p, stage);
+  e = launch_ex(paged_select_kernel<FILL>, dim3(c.Hkv + 1, c.B), kSelThreads, smem, s, 0, false, p, stage);
   if (e != cudaSuccess) return e;
   // one page per CTA until every SM has its fill of them, then up to four
   const long long ctas = 2ll * p.keep * c.Hkv * c.B;

@@ -262,12 +262,16 @@ __global__ void __launch_bounds__(kStepThreads, 2)
   if (warp == kCons) {
     // ---------------------------------------------------------------- producer
     int issued = 0, scaled = 0, first = 0;  // pages copied, pages with scales, first of the batch
-    bool bad = false;
+    bool any_bad = false;
     uint64_t pol;
     asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(pol));
     for_rows([&](int b, int g, int4 st, int i0, int i1) -> bool {
       const int32_t* const tab = c.table + ((long long)b * c.Hkv + g) * c.cap;
       const int end = min(i1, st.x);
+      // a head whose page numbers are not all in order, that of a full tail's page among them, gives
+      // nothing (paged_finish_kernel): what page 0 stands in for is another row's
+      bool bad = false;
+      const int next_page = i1 == st.x + 1 && st.y == kTile - 1 ? tab[st.x] : 0;  // (looked at last)
       // page numbers and scales 32 at a time, a batch ahead
       int page = 0;
       float2 sc = make_float2(0.0f, 0.0f);
@@ -308,9 +312,17 @@ __global__ void __launch_bounds__(kStepThreads, 2)
         }
         first = scaled;
       }
+      bad = __any_sync(0xffffffffu, bad || next_page < 0 || next_page >= c.n_pool);
+      if (lane == 0) {
+        int32_t* const slot = p.bad + blockIdx.x + b * c.Hkv + g;
+        slot[0] = bad;
+        // the next row's, or, where the piece ends with the row, nobody's: a sequence is read as a whole
+        if (i1 == st.x + 1) slot[1] = 0;
+      }
+      any_bad |= bad;
       return true;
     });
-    if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(p.status, TRA_DEV_BAD_CACHE);
+    if (any_bad && lane == 0) atomicOr(p.status, TRA_DEV_BAD_CACHE);
     // an abandoned piece: every copy lands before the CTA leaves
     if (*err) {
       for (; scaled < issued; ++scaled)
@@ -619,6 +631,7 @@ __global__ void __launch_bounds__(kFinThreads, 8) paged_finish_kernel(const Page
   grid_wait();
   const int4 st = p.ws_state[b];
   const int2 info = p.row_info[row];
+  const int last = p.row_info[row - g + c.Hkv - 1].y;  // last piece of the sequence
   const long long row64 = (long long)row * (c.cap + 1) * kTile;
   const int tok = st.x * kTile + st.y;  // tokens before the step
   // the row's chunk per CTA: whatever the cache's capacity, its tokens are spread over the grid
@@ -639,6 +652,18 @@ __global__ void __launch_bounds__(kFinThreads, 8) paged_finish_kernel(const Page
   const int chunks = (total + chunk - 1) / chunk;
   const long long slot0 = (long long)info.x + row;
   const int cnt = info.y - info.x + 1;
+  // Page numbers out of range: of this head (its output and weights stay), and, for the one CTA that
+  // writes the state, of any head of the sequence (the state stays).  A sequence's slots follow one
+  // another, with zeroes between.
+  const bool writes_state = x == 0 && g == 0;
+  const int all = writes_state ? last + c.Hkv - info.x : cnt;
+  const int bad_first = t < all ? p.bad[slot0 + t] : 0;  // (on its way during the heads' loop)
+  int bad_here = 0, bad_any = 0;
+  for (int i = t + kFinThreads; i < all; i += kFinThreads) {
+    const int v = p.bad[slot0 + i];
+    if (i < cnt) bad_here |= v;
+    bad_any |= v;
+  }
   for (int h = warp; h < grp; h += kFinThreads / 32) {
     float M = -INFINITY, L = 0.0f;
     for (int i = lane; i < cnt; i += 32) {  // running maximum and sum over this lane's pieces
@@ -666,7 +691,19 @@ __global__ void __launch_bounds__(kFinThreads, 8) paged_finish_kernel(const Page
       s_w[h * kPieces + i] = m == -INFINITY ? 0.0f : ex2(m - MM) * il;
     }
   }
-  __syncthreads();
+  const bool stays = __syncthreads_or(bad_here | (t < cnt ? bad_first : 0));
+  if (writes_state) {
+    const bool same = __syncthreads_or(bad_any | bad_first);
+    if (t == 0)
+      reinterpret_cast<int4*>(p.state_out)[b] =
+          same ? st : make_int4(st.x + (st.y == kTile - 1), (st.y + 1) % kTile, st.z + 1, st.w);
+  }
+  if (stays) {
+    if (p.weight_out != c.weight)
+      for (long long i = (long long)x * chunk + t; i < tok && i < (long long)(x + 1) * chunk; i += kFinThreads)
+        p.weight_out[row64 + i] = c.weight[row64 + i];
+    return;
+  }
 
   // outputs of heads x, x + chunks, ...: a warp takes every fourth piece, then they are joined
   for (int gg = x; gg < grp; gg += chunks) {
@@ -735,12 +772,9 @@ __global__ void __launch_bounds__(kFinThreads, 8) paged_finish_kernel(const Page
       p.weight_out[row64 + i] = old[k] + w;
     }
   }
-  if (x != 0) return;
-  if (st.y == kTile - 1) {  // the tail is full: the row's next page
+  if (x == 0 && st.y == kTile - 1) {  // the tail is full: the row's next page
     const int page = c.table[(long long)row * c.cap + st.x];
-    if (page < 0 || page >= c.n_pool) {
-      if (t == 0) atomicOr(p.status, TRA_DEV_BAD_CACHE);
-    } else {
+    if (page >= 0 && page < c.n_pool) {  // (a step whose waits ran out may have left no mark)
       const uint16_t* const kt = c.k_tail + (long long)row * kTile * D;
       const uint16_t* const vt = c.v_tail + (long long)row * kTile * D;
       const long long at = (long long)page * kTile * D;
@@ -748,9 +782,6 @@ __global__ void __launch_bounds__(kFinThreads, 8) paged_finish_kernel(const Page
       quantise_page<D, kFinThreads>([&](int r) { return vt + r * D; }, c.v8 + at, c.sv + page, s_red + kFinThreads / 32);
     }
   }
-  if (g == 0 && t == 0)
-    reinterpret_cast<int4*>(p.state_out)[b] =
-        make_int4(st.x + (st.y == kTile - 1), (st.y + 1) % kTile, st.z + 1, st.w);
 }
 
 template <int D, int GRP, bool SPLIT>
@@ -799,7 +830,8 @@ PagedLayout paged_layout(const tra_paged_cache& c) {
   l.state = 0;
   const size_t head = up((size_t)c.B * 16);
   l.info = head;
-  l.ml = l.info + up(rows * 8);
+  l.bad = l.info + up(rows * 8);
+  l.ml = l.bad + up(slots * 4);
   l.o = l.ml + up(slots * grp * 8);
   l.scores = l.o + up(slots * grp * c.d * 4);
   const size_t step_end = l.scores + up(rows * (c.cap + 1) * kTile * paged_score_stride((int)grp) * 4);

@@ -956,6 +956,7 @@ tra_status paged_attention_decode(const tra_paged_cache* cache, const uint16_t* 
   p.status = status_dev;
   p.ws_state = reinterpret_cast<int4*>(ws + lay.state);
   p.row_info = reinterpret_cast<int2*>(ws + lay.info);
+  p.bad = reinterpret_cast<int32_t*>(ws + lay.bad);
   p.part_ml = reinterpret_cast<float*>(ws + lay.ml);
   p.part_o = reinterpret_cast<float*>(ws + lay.o);
   p.scores = reinterpret_cast<float*>(ws + lay.scores);

@@ -220,6 +220,7 @@ struct PagedStepParams {
   float* part_ml;        // [pieces][grp][2]
   float* part_o;         // [pieces][grp][d]
   float* scores;         // [B][Hkv][(cap + 1) * 64][paged_score_stride(grp)]
+  int32_t* bad;          // [pieces + rows] a (piece, row) met a page number out of range
 };
 
 struct PagedMaps {
@@ -251,7 +252,7 @@ struct PagedCutParams {
 };
 
 struct PagedLayout {     // byte offsets in the workspace
-  size_t state, ml, o, scores, info, src, dst, weight, pos, total;
+  size_t state, ml, o, scores, info, bad, src, dst, weight, pos, total;
 };
 PagedLayout paged_layout(const tra_paged_cache& c);
 // floats per token in the score array: the group's heads, an even number above one
