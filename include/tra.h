@@ -559,6 +559,13 @@ TRA_API tra_status paged_cache_evict(const tra_paged_cache* cache, int32_t keep,
                                      int32_t* pos_out, void* workspace, size_t workspace_bytes,
                                      int32_t* status_dev, void* stream);
 
+/* The same for the rows of more than `keep` pages that hold at least `least` tokens, pages and
+ * tail together; the others stay.  least >= 0. */
+TRA_API tra_status paged_cache_evict_from(const tra_paged_cache* cache, int32_t keep, int32_t least,
+                                          int32_t recent, int32_t* state_out, int32_t* table_out,
+                                          float* weight_out, int32_t* pos_out, void* workspace,
+                                          size_t workspace_bytes, int32_t* status_dev, void* stream);
+
 /* Complete-tile counts of one head's boundary pair over a batch (TriAttention
  * abstract: candidate boundary pairs are weighed by complete-tile execution costs):
  * n8 = sum over every sequence's q-tiles qt of min(qt + 1, b1), n4 = the sum of

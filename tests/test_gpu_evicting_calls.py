@@ -242,3 +242,129 @@ def test_step_with_a_bad_page_in_a_long_list(pages):
         for r, (n, _) in enumerate(rows):
             want = state[r, :2].tolist() if r == b else [n + 1, 0]
             assert cache["state"][r, :2].tolist() == want, (b, r)
+
+
+# ================================================================ which rows are cut
+@pytest.mark.parametrize("least,cut", [(0, (0, 1, 3)), (4 * TILE + 63, (1, 3)), (4 * TILE + 64, (3,)), (2 ** 31 - 1, ())])
+@pytest.mark.parametrize("apart", [False, True], ids=["in place", "apart"])
+def test_evict_from(least, cut, apart):
+    """Rows below `least` tokens stay, whatever they hold."""
+    rows = [(4, 62), (4, 63), (2, 63), (5, 0), (-1, 3)]
+    cache, _ = _filled(rows, 4, 2, 64, 8, seed=7)
+    before, ref = _copy(cache), Mirror(cache)
+    for b in range(len(rows)):      # to the mirror, the others are idle
+        if b not in cut:
+            ref.t["state"][b, 0] = -1
+    ref.evict(2, 30)
+    for b in range(len(rows)):
+        if b not in cut:
+            ref.t["state"][b, 0] = rows[b][0]
+    outs = {n + "_out": torch.full_like(cache[n], -5) for n in ("state", "table", "weight", "pos")} if apart else {}
+    tra.paged_cache_evict(cache, keep=2, recent=30, least=least, **outs)
+    assert int(cache.status) == 0
+    if not apart:
+        ref.same()
+        return
+    assert all(torch.equal(cache[n], before[n]) for n in ("state", "table", "weight", "pos", "k_tail", "v_tail"))
+    ref.same("k8", "v8", "sk", "sv")
+    assert np.array_equal(outs["state_out"].cpu().numpy(), ref.t["state"])
+    assert np.array_equal(outs["table_out"].cpu().numpy(), ref.t["table"])
+    for b in range(4):
+        m = ref.t["state"][b, 0] * TILE + rows[b][1]
+        for n in ("weight", "pos"):
+            assert np.array_equal(outs[n + "_out"][b, :, :m].cpu().numpy(), ref.t[n][b, :, :m]), (b, n)
+
+
+def _plan_steps(lens, which, seed, n, **kw):
+    """A plan over the sequences `which` of a batch, n steps; per sequence its outputs, positions and
+    weights after each step in which a row was cut, and the pages that every row had at every step."""
+    hq, hkv, d = 4, 2, 64
+    parts = []
+    for i, T in enumerate(lens):
+        gen = _rng(seed + i)
+        parts.append([_normal(gen, T, h, d) for h in (hq, hkv, hkv)] + [[_normal(gen, n, h, d) for h in (hq, hkv, hkv)]])
+    q, k, v = (torch.cat([parts[i][x] for i in which]) for x in range(3))
+    shape = tra.Shape(_cu([lens[i] for i in which]), hq, hkv, d)
+    plan = api.EvictingDecodePlan(shape, keep=2, limit=4, recent=70, **kw)
+    plan.prefill(q, k, v)
+    outs, pages = [], []
+    for s in range(n):
+        x = [torch.stack([parts[i][3][y][s] for i in which]) for y in range(3)]
+        out = torch.empty_like(x[0])
+        plan.step(*x, out)
+        outs.append(out)
+        pages.append([r[0] for r in plan.rows])
+        assert plan.cache["state"][:, :2].cpu().tolist() == plan.rows
+    assert int(plan.status) == 0
+    return plan, torch.stack(outs), pages
+
+
+def test_a_row_is_cut_alike_alone_and_beside_others():
+    """With per_row a row's cuts, and so the tokens that it holds, are its own; without, the longest
+    row's cuts are everybody's.  (Outputs: the batch changes how a row is split, its fp32 sums' order and a
+    bf16 rounding, 2^-8 of values up to 4.)"""
+    lens, n = [300, 130, 64], 330
+    plan, outs, pages = _plan_steps(lens, (0, 1, 2), 40, n, per_row=True)
+    cuts = [[s for s in range(1, n) if pages[s][b] < pages[s - 1][b]] for b in range(3)]
+    assert all(cuts) and cuts[0] != cuts[1] != cuts[2]
+    for b in range(3):
+        alone, o, p = _plan_steps(lens, (b,), 40, n, per_row=True)
+        assert [x[0] for x in p] == [x[b] for x in pages]
+        m = pages[-1][b] * TILE + plan.rows[b][1]
+        assert torch.equal(alone.cache["pos"][0, :, :m], plan.cache["pos"][b, :, :m])
+        assert float((alone.cache["weight"][0, :, :m] - plan.cache["weight"][b, :, :m]).abs().max()) < 1e-3
+        assert float((o[:, 0].float() - outs[:, b].float()).abs().max()) <= 2.0 ** -6
+    _, _, pages = _plan_steps(lens, (0, 1, 2), 40, n)
+    cuts = [[s for s in range(1, n) if pages[s][b] < pages[s - 1][b]] for b in range(3)]
+    assert cuts[0][0] in cuts[1] and cuts[0][0] in cuts[2]
+
+
+def test_retired_row():
+    """A row that is done keeps what it holds, gets no output and causes no cut of the others."""
+    hq, hkv, d, lens = 4, 2, 64, [190, 64]
+    gen, cu = _rng(51), _cu(lens)
+    q, k, v = (_normal(gen, cu[-1], h, d) for h in (hq, hkv, hkv))
+    plan = api.EvictingDecodePlan(tra.Shape(cu, hq, hkv, d), keep=1, limit=2, recent=10)
+    plan.prefill(q, k, v)
+    plan.retire(0)
+    held = _copy(plan.cache)
+    for i in range(80):
+        x = [_normal(gen, 2, h, d) for h in (hq, hkv, hkv)]
+        out = torch.full_like(x[0], 5.0)
+        plan.step(*x, out)
+        assert bool((out[0] == 5.0).all()) and not bool((out[1] == 5.0).any())
+        assert plan.rows == [[-1, 62], [1 + (i + 1) // TILE, (i + 1) % TILE]]
+        assert plan.cache["state"][:, :2].cpu().tolist() == plan.rows
+    for n in ("state", "table", "weight", "pos", "k_tail", "v_tail"):
+        assert torch.equal(plan.cache[n][0], held[n][0]), n
+    plan.prefill(q, k, v)
+    assert plan.cache["state"][:, :2].cpu().tolist() == plan.rows == [[1, 62], [1, 0]]
+
+
+def test_captured_cut_and_step():
+    """What a plan does, captured from the calls themselves: the rows' states decide at every replay."""
+    lens, n = [300, 130], 300
+    hq, hkv, d = 4, 2, 64
+    gen, cu = _rng(61), _cu(lens)
+    q, k, v = (_normal(gen, cu[-1], h, d) for h in (hq, hkv, hkv))
+    x = [_normal(gen, 2, h, d) for h in (hq, hkv, hkv)]
+    shape = tra.Shape(cu, hq, hkv, d)
+    plans = [api.EvictingDecodePlan(shape, keep=2, limit=4, recent=70, per_row=True) for _ in range(2)]
+    outs = [torch.empty_like(x[0]) for _ in plans]
+    for p in plans:
+        p.prefill(q, k, v)
+    tra.paged_cache_evict(plans[0].cache, keep=4, least=2 ** 30)     # loads the kernels, cuts nothing
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=torch.cuda.Stream()):
+        tra.paged_cache_evict(plans[0].cache, keep=2, recent=70, least=4 * TILE + 63)
+        tra.paged_attention_decode(plans[0].cache, *x, outs[0], softmax_scale=0.125)
+    for i in range(n):
+        for y, z in zip(x, (hq, hkv, hkv)):
+            y.copy_(_normal(_rng(100 + i), 2, z, d))
+        g.replay()
+        plans[1].step(*x, outs[1], scale=0.125)
+        assert torch.equal(*outs), i
+    for name in plans[0].cache.NAMES:
+        assert torch.equal(plans[0].cache[name], plans[1].cache[name]), name
+    assert int(plans[0].status) == 0

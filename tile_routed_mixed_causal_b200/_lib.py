@@ -107,6 +107,7 @@ def load():
         "paged_cache_fill": ([P, P, P, P, P, I32, I32, P, SZ, P, P], I32),
         "paged_attention_decode": ([P, P, P, P, F, P, P, P, P, SZ, P, P], I32),
         "paged_cache_evict": ([P, I32, I32, P, P, P, P, P, SZ, P, P], I32),
+        "paged_cache_evict_from": ([P, I32, I32, I32, P, P, P, P, P, SZ, P, P], I32),
     }
     for name, (args, res) in sig.items():
         fn = getattr(lib, name)
@@ -499,13 +500,13 @@ def paged_attention_decode(cache: PagedCache, q, k_new, v_new, out, *, softmax_s
                                          *cache._scratch, _stream(stream)))
 
 
-def paged_cache_evict(cache: PagedCache, *, keep: int, recent: int = 0, state_out=None, table_out=None,
-                      weight_out=None, pos_out=None, stream=None):
-    """Every row of more than `keep` pages is cut to that many (include/tra.h).  The outputs: all
-    four or none (in place)."""
+def paged_cache_evict(cache: PagedCache, *, keep: int, recent: int = 0, least: int = 0, state_out=None,
+                      table_out=None, weight_out=None, pos_out=None, stream=None):
+    """Every row of more than `keep` pages that holds at least `least` tokens is cut to that many pages
+    (include/tra.h).  The outputs: all four or none (in place)."""
     _launch_device(cache.t["k8"])
-    _check(load().paged_cache_evict(
-        cache.c, int(keep), int(recent), cache._out("state", state_out), cache._out("table", table_out),
+    _check(load().paged_cache_evict_from(
+        cache.c, int(keep), int(least), int(recent), cache._out("state", state_out), cache._out("table", table_out),
         cache._out("weight", weight_out), cache._out("pos", pos_out), *cache._scratch, _stream(stream)))
 
 

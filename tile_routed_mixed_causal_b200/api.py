@@ -9,7 +9,7 @@ and recent tokens).
 ``HybridPrefillPlan``: quantize_qkv_tiles (K and V INT4 scales) ->
 hybrid_select_tokens -> hybrid_attention_prefill.
 ``EvictingDecodePlan``: attention_weight_sums -> paged_cache_fill (once, over the prompt)
--> paged_attention_decode per step, with paged_cache_evict whenever a row reaches its limit.
+-> paged_attention_decode per step, with paged_cache_evict whenever a row has no room.
 ``prompt_importance``: attention_weight_sums as the importance of a hybrid selection.
 Buffers are allocated once per plan; ``run``/``step`` only enqueue kernels.  The
 decode workspace is zero-filled once (the decode's arrival counters need that, and
@@ -171,16 +171,23 @@ def prompt_importance(shape: L.Shape, q, k, n_queries: int = 64, lse=None, scale
 
 
 class EvictingDecodePlan:
-    """Decoding over a bounded INT8 cache: every row keeps `keep` pages of its prompt and grows
-    to `limit` pages, then its tokens of least accumulated attention weight go until `keep`
-    pages are left (the last `recent` tokens always stay)."""
+    """Decoding over a bounded INT8 cache: every row keeps at most `keep` pages of its prompt and
+    grows to at most `limit` pages.  When a row there has no room for its next page, rows are cut:
+    their tokens of least accumulated attention weight go until `keep` pages are left (the last
+    `recent` tokens stay).  Cut are all rows of more than `keep` pages, which makes cuts rare, but lets
+    what a row keeps depend on the rows beside it; with per_row only those without room, so that
+    a row keeps what it would keep alone.
+
+    The plan counts its rows on the host, as step() is called.  A captured step is counted
+    once, however often it is replayed: capture paged_cache_evict (its `least` lets the rows' own
+    states decide) and paged_attention_decode for that."""
 
     def __init__(self, shape: L.Shape, keep: int, limit: int, recent: int = 64, n_queries: int = 64,
-                 device="cuda"):
+                 device="cuda", per_row: bool = False):
         if not 1 <= keep < limit:
             raise ValueError(f"need 1 <= keep < limit (got {keep}, {limit})")
         self.shape, self.keep, self.limit = shape, keep, limit
-        self.recent, self.n_queries = recent, n_queries
+        self.recent, self.n_queries, self.per_row = recent, n_queries, per_row
         # an eviction writes its `keep` pages beside the row's own
         self.cache = L.PagedCache(shape.B, shape.Hq, shape.Hkv, shape.d, limit + keep, device=device)
         self.rows = None        # [pages, tail] of each row, as the device has them
@@ -201,14 +208,26 @@ class EvictingDecodePlan:
         return w
 
     def step(self, q, k_new, v_new, out, scale=None, stream=None):
-        """One decoded token per row; rows that have no room for its page are cut first."""
+        """One decoded token per row; where one has no room for its page, rows are cut first."""
         if self.rows is None:
             raise RuntimeError("step() needs a prompt: call prefill() first")
         scale = 1.0 / math.sqrt(self.shape.d) if scale is None else scale
-        if any(n >= self.limit and t == L.TILE - 1 for n, t in self.rows):
-            L.paged_cache_evict(self.cache, keep=self.keep, recent=self.recent, stream=stream)
+        no_room = self.limit * L.TILE + L.TILE - 1     # tokens of such a row
+        if any(n * L.TILE + t >= no_room for n, t in self.rows):
+            least = no_room if self.per_row else 0
+            L.paged_cache_evict(self.cache, keep=self.keep, recent=self.recent, least=least, stream=stream)
             for r in self.rows:
-                r[0] = min(r[0], self.keep)
+                if r[0] * L.TILE + r[1] >= least:
+                    r[0] = min(r[0], self.keep)
         L.paged_attention_decode(self.cache, q, k_new, v_new, out, softmax_scale=scale, stream=stream)
         for r in self.rows:
-            r[0], r[1] = r[0] + (r[1] == L.TILE - 1), (r[1] + 1) % L.TILE
+            if r[0] >= 0:
+                r[0], r[1] = r[0] + (r[1] == L.TILE - 1), (r[1] + 1) % L.TILE
+
+    def retire(self, b: int, stream=None):
+        """Row b is done: later steps leave it, its output and the other rows' cuts alone."""
+        if self.rows is None:
+            raise RuntimeError("retire() needs a prompt: call prefill() first")
+        with _made_on(stream, self.cache.device):
+            self.cache["state"][b, 0] = -1
+        self.rows[b][0] = -1

@@ -67,9 +67,12 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* tmp, uint32
   return tmp[warp] + s - v;
 }
 
-// Evict: the row is to be cut, and has the free pages for it.
+// Evict: the row is to be cut; and has the free pages for it.
+__device__ __forceinline__ bool cut_due(const PagedCutParams& p, int4 st) {
+  return paged_row(st, p.c.cap) == kRowOk && st.x > p.keep && st.x * kTile + st.y >= p.least;
+}
 __device__ __forceinline__ bool cut_fits(const PagedCutParams& p, int4 st) {
-  return paged_row(st, p.c.cap) == kRowOk && st.x > p.keep && st.x <= p.c.cap - p.keep;
+  return cut_due(p, st) && st.x <= p.c.cap - p.keep;
 }
 
 // What becomes of row b, for the kernels behind the selection: the CTA beside those of its heads.
@@ -94,7 +97,7 @@ __device__ __forceinline__ void check_row(const PagedCutParams& p, int b) {
     used = cut ? s.x + p.keep : 0;
     if (threadIdx.x == 0) {
       if (kind == kRowBad) atomicOr(p.status, TRA_DEV_BAD_CACHE);
-      if (kind == kRowOk && s.x > p.keep && !cut) atomicOr(p.status, TRA_DEV_CACHE_FULL);
+      if (cut_due(p, s) && !cut) atomicOr(p.status, TRA_DEV_CACHE_FULL);
     }
   }
   bool bad = false;

@@ -974,6 +974,14 @@ tra_status paged_cache_evict(const tra_paged_cache* cache, int32_t keep, int32_t
                              int32_t* state_out, int32_t* table_out, float* weight_out,
                              int32_t* pos_out, void* workspace, size_t workspace_bytes,
                              int32_t* status_dev, void* stream) {
+  return paged_cache_evict_from(cache, keep, 0, recent, state_out, table_out, weight_out, pos_out, workspace,
+                                workspace_bytes, status_dev, stream);
+}
+
+tra_status paged_cache_evict_from(const tra_paged_cache* cache, int32_t keep, int32_t least, int32_t recent,
+                                  int32_t* state_out, int32_t* table_out, float* weight_out,
+                                  int32_t* pos_out, void* workspace, size_t workspace_bytes,
+                                  int32_t* status_dev, void* stream) {
   const CallRange range("tra::paged_cache_evict");
   tra::PagedLayout lay;
   tra_status st = check_paged(cache, workspace, workspace_bytes, status_dev, &lay);
@@ -986,12 +994,13 @@ tra_status paged_cache_evict(const tra_paged_cache* cache, int32_t keep, int32_t
   if (!aligned16(state_out) || !aligned16(table_out) || !aligned16(weight_out) || !aligned16(pos_out))
     return fail(TRA_ERR_INVALID, "state_out/table_out/weight_out/pos_out must be 16-byte aligned");
   if (keep < 1 || keep > cache->cap) return fail(TRA_ERR_INVALID, "keep must lie in [1, %d] (got %d)", cache->cap, keep);
-  if (recent < 0) return fail(TRA_ERR_INVALID, "recent must be >= 0");
+  if (recent < 0 || least < 0) return fail(TRA_ERR_INVALID, "recent and least must be >= 0");
   uint8_t* const ws = reinterpret_cast<uint8_t*>(workspace);
   tra::PagedCutParams p{};
   p.c = *cache;
   p.keep = keep;
   p.recent = recent;
+  p.least = least;
   p.nmax = (int)std::min<int64_t>((int64_t)cache->cap * TRA_TILE, 1 << 30);
   p.state_out = given ? state_out : cache->state;
   p.table_out = given ? table_out : cache->table;

@@ -233,6 +233,7 @@ struct PagedMaps {
 struct PagedCutParams {
   tra_paged_cache c;
   int keep, recent;
+  int least;             // evict: tokens from which a row is cut
   int nmax;              // most tokens of a row that are chosen among
   // fill
   const int32_t* cu;
