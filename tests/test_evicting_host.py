@@ -81,3 +81,31 @@ def test_plan_without_a_retired_row(monkeypatch, per_row):
         plan.step(None, None, None, None)
     assert calls.evicted == [] and plan.rows == [[-1, 63], [3, 3], [4, 2]]
     assert plan.cache["state"][:, 0].tolist() == [-1, 4, 4]
+
+
+@pytest.mark.parametrize("big", [2 ** 31, 2 ** 32, 2 ** 32 + 2, -2 ** 31 - 1, 10 ** 12])
+def test_numbers_past_32_bits(monkeypatch, big):
+    """They are refused, not cut off: 2^32 recent tokens are not none."""
+    tra_build.build()
+    z = lambda *s, t=torch.bfloat16: torch.zeros(s, dtype=t)  # noqa: E731
+    f32, shape = torch.float32, L.Shape([0, 128], 4, 2, 64, device="cpu")
+    cache = L.PagedCache(1, 4, 2, 64, 3, device="cpu")
+    monkeypatch.setattr(L, "_launch_device", lambda t: -1)      # as if the tensors were on a GPU
+    monkeypatch.setattr(L, "_on", lambda shape, index: None)
+    monkeypatch.setattr(L, "_stream", lambda s: None)
+
+    class Lib:
+        def __getattr__(self, name):
+            return lambda *a: pytest.fail(f"{name} was called")
+
+    monkeypatch.setattr(L, "load", lambda: Lib())
+    k = z(128, 2, 64)
+    with pytest.raises(L.TraError, match="32 bits"):
+        L.attention_weight_sums(shape, z(128, 4, 64), k, z(128, 2, t=f32), z(4, 128, t=f32), n_queries=big, softmax_scale=0.1)
+    for kw in (dict(keep=big), dict(keep=2, recent=big)):
+        with pytest.raises(L.TraError, match="32 bits"):
+            L.paged_cache_fill(cache, shape, k, k, **kw)
+        with pytest.raises(L.TraError, match="32 bits"):
+            L.paged_cache_evict(cache, **kw)
+    with pytest.raises(L.TraError, match="32 bits"):
+        L.paged_cache_evict(cache, keep=2, least=big)

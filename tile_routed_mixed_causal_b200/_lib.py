@@ -396,6 +396,13 @@ def _launch_device(t):
     return index
 
 
+def _count(name, x):
+    """x as the C call's 32-bit number; TraError where it is none (ctypes would cut it off)."""
+    if not -2 ** 31 <= int(x) < 2 ** 31:
+        raise TraError(1, f"{name} = {x} does not fit 32 bits")
+    return int(x)
+
+
 def _on(shape: Shape, index):
     if shape.cu_dev is None or shape.cu_dev.get_device() != index:
         raise TraError(1, f"the shape's cu_seqlens must be on cuda:{index}")
@@ -415,7 +422,7 @@ def attention_weight_sums(shape: Shape, q, k, weights, lse, *, n_queries: int = 
     weights = _expect("weights", weights, f32, (n, hkv), dev)
     lse = _expect("lse", lse, f32, (hq, n), dev)
     status = shape.status.data_ptr() if status is None else _expect("status", status, torch.int32, (1,), dev)
-    _check(load().attention_weight_sums(shape.c, q, k, int(n_queries), float(softmax_scale), lse, int(bool(lse_given)),
+    _check(load().attention_weight_sums(shape.c, q, k, _count("n_queries", n_queries), float(softmax_scale), lse, int(bool(lse_given)),
                                         weights, status, _stream(stream)))
 
 
@@ -430,6 +437,8 @@ class PagedCache:
     def __init__(self, B: int, Hq: int, Hkv: int, d: int, cap: int, tensors=None, device="cuda"):
         if min(B, Hq, Hkv, d, cap) < 1:
             raise TraError(1, "B, Hq, Hkv, d and cap must be >= 1")
+        for name, x in (("B", B), ("Hq", Hq), ("Hkv", Hkv), ("d", d), ("cap", cap)):
+            _count(name, x)
         self.B, self.Hq, self.Hkv, self.d, self.cap = B, Hq, Hkv, d, cap
         n_pool = B * Hkv * cap if tensors is None else int(tensors["k8"].shape[0])
         spec = {"k8": ((n_pool, TILE, d), torch.int8), "sk": ((n_pool,), torch.float32),
@@ -481,8 +490,8 @@ def paged_cache_fill(cache: PagedCache, shape: Shape, k, v, *, keep: int, recent
     v = _expect("v", v, torch.bfloat16, rows, dev)
     if weights is not None:
         weights = _expect("weights", weights, torch.float32, rows[:2], dev)
-    _check(load().paged_cache_fill(cache.c, shape.c, k, v, weights, int(keep), int(recent), *cache._scratch,
-                                   _stream(stream)))
+    _check(load().paged_cache_fill(cache.c, shape.c, k, v, weights, _count("keep", keep), _count("recent", recent),
+                                   *cache._scratch, _stream(stream)))
 
 
 def paged_attention_decode(cache: PagedCache, q, k_new, v_new, out, *, softmax_scale, state_out=None,
@@ -506,8 +515,9 @@ def paged_cache_evict(cache: PagedCache, *, keep: int, recent: int = 0, least: i
     (include/tra.h).  The outputs: all four or none (in place)."""
     _launch_device(cache.t["k8"])
     _check(load().paged_cache_evict_from(
-        cache.c, int(keep), int(least), int(recent), cache._out("state", state_out), cache._out("table", table_out),
-        cache._out("weight", weight_out), cache._out("pos", pos_out), *cache._scratch, _stream(stream)))
+        cache.c, _count("keep", keep), _count("least", least), _count("recent", recent),
+        cache._out("state", state_out), cache._out("table", table_out), cache._out("weight", weight_out),
+        cache._out("pos", pos_out), *cache._scratch, _stream(stream)))
 
 
 def boundary_tile_counts(shape: Shape, b1: int, b2: int):
