@@ -452,7 +452,8 @@ TRA_API tra_status hybrid_attention_prefill(const tra_shape* shape, const tra_hy
  * is read (the lse a prefill wrote; a row that is not finite adds nothing), otherwise the
  * window's rows are computed from q and k (dense causal) and written, and the other rows
  * are left as they were.  Products of bf16 inputs are summed in fp32, as are the weights,
- * in a fixed order: the same call gives the same bits.  q and k finite; nothing of another
+ * in a fixed order: the same call gives the same bits.  A given lse is taken as it is, not as
+ * one that shares this call's roundings.  q and k finite; nothing of another
  * sequence or of a masked pair reaches a result.  status_dev as in the prefill.
  */
 TRA_API tra_status attention_weight_sums(const tra_shape* shape, const uint16_t* q, const uint16_t* k,

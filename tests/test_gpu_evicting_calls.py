@@ -9,7 +9,7 @@ import torch
 import tile_routed_mixed_causal_b200 as tra
 from tile_routed_mixed_causal_b200 import api
 
-from test_gpu_evicting import DEV, TILE, Mirror, _cu, _filled, _normal, _rng
+from test_gpu_evicting import DEV, TILE, Mirror, _cu, _filled, _normal, _rng, _sums64
 
 pytestmark = pytest.mark.gpu
 
@@ -368,3 +368,68 @@ def test_captured_cut_and_step():
     for name in plans[0].cache.NAMES:
         assert torch.equal(plans[0].cache[name], plans[1].cache[name]), name
     assert int(plans[0].status) == 0
+
+
+# ================================================================ sums over a given lse
+def _scores_of(kind, gen, T, h, d):
+    x = torch.randn(T, h, d, generator=gen, device=DEV)
+    if kind == "whole":         # small whole numbers: every score is exact in fp32
+        return torch.randint(0, 5, (T, h, d), generator=gen, device=DEV).to(torch.bfloat16)
+    if kind == "positive":
+        x = x.abs() * 2
+    if kind == "outliers":
+        x[..., 5:9] *= 10
+    if kind == "large":
+        x *= 2.8
+    return x.to(torch.bfloat16)
+
+
+@pytest.mark.parametrize("own", [False, True], ids=["lse in 64 bits", "lse of the call"])
+@pytest.mark.parametrize("kind", ["whole", "positive", "outliers", "large", "small"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_sums_over_a_given_lse_have_no_bias(d, kind, own):
+    """All weights together against the definition with that lse, at scores up to 200: whatever the tensor
+    core cuts off must not depend on what the values are like, nor on where the lse comes from.
+
+    Bound of the mean: n = d / 16 MMAs cut a partial sum P_k - f L, L = lse / scale, off by half of its
+    last place in the mean, 0.36 * 2^-23 of it (its mantissa spread evenly over a factor of two).  With
+    f = (n + 1) / 2n these add up to nothing for a score S = L; for S < L they leave (n + 1) / 2 times
+    L - S, whose mean is the row's entropy, at most log T.  What partial sums that do not grow evenly
+    leave is taken as a quarter of all that is cut off, sum_k |k / n - f| times 2^-24 L.  Exponents and
+    sums: 2^-20.  (Without a start value it is 0.36 (n + 1) / 2 * 2^-23 L: 2e-7 L at d = 128.)"""
+    T, hq, hkv, n = 3000, 4, 2, d // 16
+    gen, scale = _rng(d), 1.0 / math.sqrt(d)
+    q, k = _scores_of(kind, gen, T, hq, d), _scores_of(kind, gen, T, hkv, d)
+    shape = tra.Shape([0, T], hq, hkv, d)
+    w, lse = torch.empty(T, hkv, device=DEV), torch.empty(hq, T, device=DEV)
+    if own:
+        tra.attention_weight_sums(shape, q, k, w, lse, softmax_scale=scale)
+    else:
+        lse.copy_(_sums64(q, k, [0, T], 0, scale)[1])
+    ref = _sums64(q, k, [0, T], 0, scale, lse)[0]
+    tra.attention_weight_sums(shape, q, k, w, lse, softmax_scale=scale, lse_given=True)
+    f = (n + 1) / (2 * n)
+    top = float(lse.abs().max())
+    uneven = 0.25 * sum(abs(i / n - f) for i in range(1, n + 1)) * 2.0 ** -24 * top
+    bound = 0.36 * 2.0 ** -23 * (n + 1) / 2 * math.log(T) + uneven + 2.0 ** -20
+    assert abs(float(w.double().sum() / ref.sum()) - 1.0) < bound
+    rel = 2.0 ** -22 * 2 * top * 1.4427 + 2.0 ** -18      # of one weight: every cut-off to one side
+    assert bool(((w.double() - ref).abs() <= rel * ref + 1e-30).all())
+
+
+@pytest.mark.parametrize("scale", [1e-30, 1e-6, 1.0, 1e6, 1e30])
+def test_sums_over_a_given_lse_at_far_scales(scale):
+    """Scales at the ends of the range, scores of ordinary size times the scale, and an lse far from
+    the scores: zeroes where the definition has them."""
+    T, hq, hkv, d = 200, 2, 1, 64
+    gen = _rng(3)
+    root = math.sqrt(1.0 / (scale * math.sqrt(d)))
+    q = (torch.randn(T, hq, d, generator=gen, device=DEV) * root).to(torch.bfloat16)
+    k = (torch.randn(T, hkv, d, generator=gen, device=DEV) * root).to(torch.bfloat16)
+    shape = tra.Shape([0, T], hq, hkv, d)
+    w = torch.empty(T, hkv, device=DEV)
+    for shift in (0.0, 1e4, 1e30, 3e38):
+        lse = (_sums64(q, k, [0, T], 0, scale)[1] + shift).float()
+        ref = _sums64(q, k, [0, T], 0, scale, lse)[0]
+        tra.attention_weight_sums(shape, q, k, w, lse, softmax_scale=scale, lse_given=True)
+        assert bool(((w.double() - ref).abs() <= 2.0 ** -17 * ref + 1e-30).all()), shift

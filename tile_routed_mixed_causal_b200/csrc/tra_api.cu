@@ -834,15 +834,8 @@ tra_status attention_weight_sums(const tra_shape* shape, const uint16_t* q, cons
   p.lse_units = (p.ragged ? q_all : q_tiles * shape->B) * (shape->Hq >> p.pack);
   p.sum_units = (p.ragged ? k_all : k_tiles * shape->B) * shape->Hkv;
   p.ntok = ntok;
-  double scale = (double)softmax_scale * 1.4426950408889634074;
-  // Against a caller's lse the scores' own bias counts: the tensor core cuts its fp32 sums off
-  // toward zero, by 1.29 (d = 128) and 0.59 (d = 64) times 2^-23 of a score in the mean (measured,
-  // with the channels taken in both orders), which the scale makes up for.  At scores near 50
-  // this and the scale in two parts bring the sums' error from 5e-6 to 2e-7.  An lse of this
-  // call's own carries the same bias, and it cancels.
-  if (lse_given) scale *= 1.0 + (shape->d == 128 ? 1.54e-7 : 7.05e-8);
-  p.scale_log2 = (float)scale;
-  p.scale_low = (float)(scale - (double)p.scale_log2);
+  p.scale_log2 = (float)((double)softmax_scale * 1.4426950408889634074);
+  p.inv_scale = 1.0 / (double)softmax_scale;
   p.lse_given = lse_given != 0;
   p.lse = lse;
   p.weights = weights;

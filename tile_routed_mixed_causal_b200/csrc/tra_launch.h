@@ -181,8 +181,8 @@ struct WeightParams {
   const int32_t* cu;
   int B, Hq, Hkv, d, n_queries;
   long long ntok;
-  float scale_log2;      // softmax_scale * log2(e),
-  float scale_low;       // and what fp32 leaves of it (sums over a given lse)
+  float scale_log2;      // softmax_scale * log2(e)
+  double inv_scale;      // 1 / softmax_scale (sums over a given lse)
   int lse_given;
   float* lse;            // [Hq][ntok]
   float* weights;        // [ntok][Hkv]

@@ -23,10 +23,17 @@
 // warps 2 and 3 stage the columns' normalisers (sums only), warps 4-7 and 8-11 take the
 // even and the odd tiles, one S block of TMEM each.
 // Sums run in fp32: within a tile over four chains, tile sums with a compensated add, so
-// that the error does not grow with the number of tiles.  Over a caller's lse the scores are
-// held closer: the scale in two parts, and the channels of every other tile multiplied in
-// reverse, so that the tensor core's truncation (largest where the large products come
-// first) has the same mean for every head and the scale can carry it.
+// that the error does not grow with the number of tiles.
+// The tensor core cuts its fp32 sums off toward zero after each of the D / 16 MMAs of a score.  An lse of
+// this call's own carries the same bias, and it cancels.  Over a caller's lse it would show (7e-6 of
+// the sums at scores near 50), so there the accumulator starts at -f L, L = lse / scale, by one more
+// MMA, of ones with the start in three bf16 parts: with f = (n + 1) / 2n of n MMAs the partial sums
+// P_k - f L of a score near L are as far below zero as above it, in the mean over both orders of the
+// channels (P_k + P'_(n-k) = L), which alternate from tile to tile; what is cut off, in proportion
+// to the sum, cancels.  What is left for the exponential, (S - f L) - (1 - f) L, is small where a
+// key has weight, so that the scale's own rounding does not show either.  Sums of 8K to 32K prompts
+// are off by 2e-7 to 7e-7 (an fp32 softmax: 2e-7 to 9e-7); the MMA costs under 1 %
+// of the time.
 // Where there are few units a cluster of up to 8 CTAs shares one (every C-th tile each)
 // and joins the partial rows over distributed shared memory in rank order: the same call
 // gives the same bits.
@@ -45,7 +52,7 @@ constexpr uint32_t kWTmemCols = 256;  // two S blocks of 128 fp32 columns
 // rescaled: the sum stays below 2^16 * 2^31
 constexpr float kLseSlack = 16.0f;
 
-template <int D>
+template <int D, bool GIVEN>
 struct WCfg {
   static constexpr int kTileBytes = kRows * D * 2;
   // tile ring: as deep as two CTAs per SM allow, or (lone) one
@@ -54,11 +61,18 @@ struct WCfg {
   static constexpr int kOffA = 0;
   static constexpr int kOffCol = kTileBytes;                        // [kColSlots][128] float
   static constexpr int kOffFlag = kOffCol + kColSlots * kRows * 4;  // [kColSlots][2] int
-  static constexpr int kOffRed = kOffFlag + kColSlots * 2 * 4;      // [2][128] float2
-  static constexpr int kOffBar = kOffRed + 2 * kRows * 8;
+  static constexpr int kOffRed = kOffFlag + kColSlots * 2 * 4;      // [2][128] float2, see red
+  static constexpr int kOffBar = kOffRed + (GIVEN ? 0 : 2 * kRows * 8);
   static constexpr int kNumBars = 1 + 2 * kStages1 + 4 + 2 * kColSlots + 1;
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;
-  static constexpr int kOffB = (kOffMisc + 32 + 1023) / 1024 * 1024;  // the ring, last
+  // over a caller's lse: 128 rows of 16 ones, and for either S block the columns' starting values
+  static constexpr int kOffX = (kOffMisc + 32 + 255) / 256 * 256;
+  static constexpr int kXBytes = kRows * 32;
+  // the rows' results of an S block's warps, at the end: over a caller's lse where its starting
+  // values were (with another place for them two CTAs per SM have no room for four column slots, and
+  // three cost 1.5 %)
+  static constexpr int red(int w) { return GIVEN ? kOffX + (1 + w) * kXBytes : kOffRed + w * kRows * 8; }
+  static constexpr int kOffB = (kOffX + (GIVEN ? 3 * kXBytes : 0) + 1023) / 1024 * 1024;  // the ring, last
   static constexpr int smem(int stages) { return kOffB + stages * kTileBytes + 1024; }
   // more than a third of an SM's shared memory each, so that no more than two CTAs share
   // one: their S blocks fill its TMEM
@@ -209,8 +223,8 @@ struct WUnit {
 template <int D, WeightPass PASS>
 __global__ void __launch_bounds__(kWThreads, 2)
     weight_kernel(const __grid_constant__ WeightParams p, const __grid_constant__ WeightMaps m) {
-  using C = WCfg<D>;
   constexpr bool LSE = PASS == kPassLse, GIVEN = PASS == kPassGiven;
+  using C = WCfg<D, GIVEN>;
   extern __shared__ uint8_t wsm_raw[];
   const uint32_t base = (smem_u32(wsm_raw) + 1023u) & ~1023u;
   uint8_t* const gbase = wsm_raw + (base - smem_u32(wsm_raw));
@@ -259,6 +273,13 @@ __global__ void __launch_bounds__(kWThreads, 2)
     mbar_init(bar_done, 1);
     *err = 0;
     fence_barrier_init();
+  }
+  if constexpr (GIVEN) {  // bf16 ones in every place of the rows' 32 bytes, zeroes in the columns'
+    for (int i = threadIdx.x; i < 3 * C::kXBytes / 16; i += kWThreads) {
+      const uint32_t v = i < C::kXBytes / 16 ? 0x3F803F80u : 0u;
+      reinterpret_cast<uint4*>(gbase + C::kOffX)[i] = make_uint4(v, v, v, v);
+    }
+    fence_proxy_async_smem();
   }
   if (warp == 1) {
     tmem_alloc(smem_u32(tmem_slot), kWTmemCols);
@@ -309,13 +330,17 @@ __global__ void __launch_bounds__(kWThreads, 2)
       // S block w last held tile n - 2; its warps have read it into registers
       if (n >= 2 && !wwait(bar_sfree(w), ((n >> 1) - 1) & 1)) break;
       if (!wwait(bar_bfull(s), (n / stages) & 1)) break;
+      if (GIVEN && !wwait(bar_cfull(n % kColSlots), (n / kColSlots) & 1)) break;
       tc_fence_after();
+      if (GIVEN)  // the starting values
+        mma_bf16_e(tmem + w * kRows, smem_desc(base + C::kOffX, 16, 256, kSwz32),
+                   smem_desc(base + C::kOffX + (1 + w) * C::kXBytes, 16, 256, kSwz32), kId, 0u);
       const uint64_t dB = smem_desc(base + C::kOffB + s * C::kTileBytes, 16, 1024, kSwz128);
 #pragma unroll
       for (int i = 0; i < D / 16; ++i) {  // 16 channels: 32 bytes within a 64-channel slab of 16 KB
         const int kk = GIVEN && (n & 1) ? D / 16 - 1 - i : i;
         const uint32_t off = (kk >> 2) * 1024 + (kk & 3) * 2;
-        mma_bf16_e(tmem + w * kRows, dA + off, dB + off, kId, i > 0 ? 1u : 0u);
+        mma_bf16_e(tmem + w * kRows, dA + off, dB + off, kId, GIVEN || i > 0 ? 1u : 0u);
       }
       mma_commit_e(bar_bfree(s));
       mma_commit_e(bar_sfull(w));
@@ -331,21 +356,42 @@ __global__ void __launch_bounds__(kWThreads, 2)
       const int c = (warp - 2) * 64 + lane;  // and c + 32
       for (int n = 0; n < nsteps; ++n) {
         const int s = n % kColSlots, use = n / kColSlots;
-        if (use > 0 && !wwait(bar_cfree(s), (use - 1) & 1)) break;
         int h, x0;
         x.column(p, (int)rank + n * (int)nrank, h, x0);
         const float* const src = p.lse + (long long)h * p.ntok + x.seq0;
-        bool odd = false;
+        float z[2];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           const int i = x0 + ((c + 32 * k) >> p.pack);
-          const float z = i < x.T ? src[((c + 32 * k) & ((1 << p.pack) - 1)) * p.ntok + i] : INFINITY;
-          const bool fin = isfinite(z);  // a row that is not finite adds nothing
+          z[k] = i < x.T ? src[((c + 32 * k) & ((1 << p.pack) - 1)) * p.ntok + i] : INFINITY;
+        }
+        if (use > 0 && !wwait(bar_cfree(s), (use - 1) & 1)) break;
+        // the starting values' tile was last read by the MMAs of tile n - 2
+        if (GIVEN && n >= 2 && !wwait(bar_sfull(n & 1), ((n >> 1) - 1) & 1)) break;
+        bool odd = false;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const bool fin = isfinite(z[k]);  // a row that is not finite adds nothing
           odd |= !fin;
-          col[s * kRows + c + 32 * k] = fin ? z * -1.4426950408889634f : -INFINITY;
+          float v = z[k] * -1.4426950408889634f;
+          if constexpr (GIVEN) {
+            constexpr int kMmas = D / 16;
+            const double L = fin ? (double)z[k] * p.inv_scale : 0.0;
+            // (beyond 2^60 every exponential is zero or infinite)
+            const float a = fminf(fmaxf((float)(L * (-0.5 * (kMmas + 1) / kMmas)), -0x1p60f), 0x1p60f);
+            v = (float)((-(double)a - L) * (double)p.scale_log2);
+            // a in three bf16 parts, exactly
+            const __nv_bfloat16 hi = __float2bfloat16_rn(a);
+            const float r = a - __bfloat162float(hi);
+            const __nv_bfloat162 lo = __floats2bfloat162_rn(r, r - __bfloat162float(__float2bfloat16_rn(r)));
+            *reinterpret_cast<uint2*>(gbase + C::kOffX + (1 + (n & 1)) * C::kXBytes + (c + 32 * k) * 32) =
+                make_uint2(*reinterpret_cast<const uint16_t*>(&hi), *reinterpret_cast<const uint32_t*>(&lo));
+          }
+          col[s * kRows + c + 32 * k] = fin ? v : -INFINITY;
         }
         odd = __any_sync(0xffffffffu, odd);
         if (lane == 0) flag[s * 2 + warp - 2] = odd;
+        if (GIVEN) fence_proxy_async_smem();
         __syncwarp();
         mbar_arrive(bar_cfull(s));
       }
@@ -357,7 +403,7 @@ __global__ void __launch_bounds__(kWThreads, 2)
     const int row = x.r0 + (LSE ? r >> p.pack : r);   // query or key position
     const uint32_t tS = tmem + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)(w * kRows);
     const float c1 = p.scale_log2;
-    const float2 c2 = make_float2(c1, c1), c2l = make_float2(p.scale_low, p.scale_low);
+    const float2 c2 = make_float2(c1, c1);
     const bool warp_rows = x.r0 + ((warp & 3) * 32 >> (LSE ? p.pack : 0)) < x.T;
     float total = 0.0f, comp = 0.0f;                  // sums: compensated total
     float mref = -INFINITY, l = 0.0f;                 // lse
@@ -451,11 +497,7 @@ __global__ void __launch_bounds__(kWThreads, 2)
               const float4 z = nl[(c0 + k) / 4];
               const float2 s0 = make_float2(__uint_as_float(sr[k]), __uint_as_float(sr[k + 1]));
               const float2 s1 = make_float2(__uint_as_float(sr[k + 2]), __uint_as_float(sr[k + 3]));
-              float2 e0 = __ffma2_rn(s0, c2, make_float2(z.x, z.y)), e1 = __ffma2_rn(s1, c2, make_float2(z.z, z.w));
-              if (GIVEN) {
-                e0 = __ffma2_rn(s0, c2l, e0);
-                e1 = __ffma2_rn(s1, c2l, e1);
-              }
+              const float2 e0 = __ffma2_rn(s0, c2, make_float2(z.x, z.y)), e1 = __ffma2_rn(s1, c2, make_float2(z.z, z.w));
               a[0] = __fadd2_rn(a[0], make_float2(ex2(e0.x), ex2(e0.y)));
               a[1] = __fadd2_rn(a[1], make_float2(ex2(e1.x), ex2(e1.y)));
             }
@@ -476,8 +518,7 @@ __global__ void __launch_bounds__(kWThreads, 2)
               float e[4];
 #pragma unroll
               for (int y = 0; y < 4; ++y) {
-                const float sy = __uint_as_float(sr[k + y]), x = fmaf(sy, c1, zz[y]);
-                e[y] = ex2(GIVEN ? fmaf(sy, p.scale_low, x) : x);
+                e[y] = ex2(fmaf(__uint_as_float(sr[k + y]), c1, zz[y]));
                 if (k + y < lim || zz[y] == -INFINITY) e[y] = 0.0f;
               }
               a[0] = __fadd2_rn(a[0], make_float2(e[0], e[1]));
@@ -498,7 +539,7 @@ __global__ void __launch_bounds__(kWThreads, 2)
       }
     }
     part = LSE ? make_float2(mref, l) : make_float2(total, 0.0f);
-    reinterpret_cast<float2*>(gbase + C::kOffRed)[w * kRows + r] = part;
+    reinterpret_cast<float2*>(gbase + C::red(w))[r] = part;
   }
   tc_fence_before();
   __syncthreads();
@@ -510,14 +551,14 @@ __global__ void __launch_bounds__(kWThreads, 2)
   if (nrank > 1) cluster_sync();
   const int row = x.r0 + (LSE ? (int)threadIdx.x >> p.pack : (int)threadIdx.x);
   if (rank == 0 && threadIdx.x < kRows && row < x.T) {
-    const uint32_t red = base + C::kOffRed + threadIdx.x * 8;
+    const uint32_t red = base + threadIdx.x * 8;
     float mm = -INFINITY, acc = 0.0f;
     if (LSE)
       for (uint32_t k = 0; k < nrank; ++k)
-        for (uint32_t w = 0; w < 2; ++w) mm = fmaxf(mm, ld_cluster_f2(red + w * kRows * 8, k).x);
+        for (int w = 0; w < 2; ++w) mm = fmaxf(mm, ld_cluster_f2(red + C::red(w), k).x);
     for (uint32_t k = 0; k < nrank; ++k)
-      for (uint32_t w = 0; w < 2; ++w) {
-        const float2 v = ld_cluster_f2(red + w * kRows * 8, k);
+      for (int w = 0; w < 2; ++w) {
+        const float2 v = ld_cluster_f2(red + C::red(w), k);
         if (LSE) acc += v.x == -INFINITY ? 0.0f : v.y * ex2(v.x - mm);
         else acc += v.x;
       }
@@ -532,7 +573,7 @@ __global__ void __launch_bounds__(kWThreads, 2)
 
 template <int D, WeightPass PASS>
 cudaError_t launch_weight_pass(WeightParams p, const WeightMaps& m, bool overlap, cudaStream_t s) {
-  using C = WCfg<D>;
+  using C = WCfg<D, PASS == kPassGiven>;
   constexpr bool LSE = PASS == kPassLse;
   const long long units = LSE ? p.lse_units : p.sum_units, longest = LSE ? p.lse_longest : p.sum_longest;
   // CTAs per unit: as few as bring the longest unit near the mean load of the grid's 296
