@@ -433,3 +433,23 @@ def test_sums_over_a_given_lse_at_far_scales(scale):
         ref = _sums64(q, k, [0, T], 0, scale, lse)[0]
         tra.attention_weight_sums(shape, q, k, w, lse, softmax_scale=scale, lse_given=True)
         assert bool(((w.double() - ref).abs() <= 2.0 ** -17 * ref + 1e-30).all()), shift
+
+
+@pytest.mark.parametrize("T", [200, 3000])
+def test_infinite_sums(T):
+    """An lse far below the scores: sums past fp32's range are infinite, not NaN, key by key."""
+    hq, hkv, d = 2, 1, 64
+    gen = _rng(4)
+    q, k = _normal(gen, T, hq, d), _normal(gen, T, hkv, d)
+    shape = tra.Shape([0, T], hq, hkv, d)
+    lse = _sums64(q, k, [0, T], 0, 0.125)[1].float()
+    w = torch.empty(T, hkv, device=DEV)
+    lse[0, T // 2] = -1e5           # one query: the keys up to it are seen by it
+    ref = _sums64(q, k, [0, T], 0, 0.125, lse)[0]
+    assert bool(torch.isinf(ref[:T // 2 + 1]).all()) and bool(torch.isfinite(ref[T // 2 + 1:]).all())
+    tra.attention_weight_sums(shape, q, k, w, lse, softmax_scale=0.125, lse_given=True)
+    assert bool((w[:T // 2 + 1] == math.inf).all())
+    assert bool(((w.double() - ref)[T // 2 + 1:].abs() <= 2.0 ** -17 * ref[T // 2 + 1:]).all())
+    lse -= 1e5
+    tra.attention_weight_sums(shape, q, k, w, lse, softmax_scale=0.125, lse_given=True)
+    assert bool((w == math.inf).all())

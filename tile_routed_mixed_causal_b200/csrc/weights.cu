@@ -530,7 +530,7 @@ __global__ void __launch_bounds__(kWThreads, 2)
         // compensated add: comp carries what the total could not hold
         const float y = __fsub_rn(s2.x + s2.y, comp);
         const float t = __fadd_rn(total, y);
-        comp = __fsub_rn(__fsub_rn(t, total), y);
+        comp = t < INFINITY ? __fsub_rn(__fsub_rn(t, total), y) : 0.0f;  // (an infinite sum stays one)
         total = t;
       }
       if (!LSE) {
