@@ -519,7 +519,8 @@ TRA_API tra_status paged_cache_fill(const tra_paged_cache* cache, const tra_shap
 /*
  * paged_attention_decode -- one token per row: every query head attends to its KV head's
  * pages (K = s * code, V = s * code), tail and the new token; one softmax per head with
- * queries in bf16, scores and statistics in fp32.  out bf16 [B][Hq][d].  Then
+ * queries in bf16, scores and statistics in fp32; the probabilities meet V in two f16 parts
+ * (pages, 22 bits) or two bf16 parts (tail, 16 bits), summed in fp32.  out bf16 [B][Hq][d].  Then
  *   weight[b][g][i] += the sum of the group's probabilities of token i (the new token's
  *   starts from zero), pos of the new token = seen, the token is appended to the tail and
  *   seen grows by one; a tail of 64 tokens is quantised into page table[b][g][n_pages] and

@@ -453,3 +453,30 @@ def test_infinite_sums(T):
     lse -= 1e5
     tra.attention_weight_sums(shape, q, k, w, lse, softmax_scale=0.125, lse_given=True)
     assert bool((w == math.inf).all())
+
+
+# ================================================================ probabilities against V
+@pytest.mark.parametrize("cap", [5, 700])
+@pytest.mark.parametrize("d", [64, 128])
+def test_values_that_cancel(d, cap):
+    """Eight tokens of a row have values, of either sign: where they cancel, what P is rounded to shows past the
+    output's own rounding.  Bounds: the output's bf16, half a step 2^-8; of the sum of p |v|: exponents (|q| |k|
+    in fp32, 2 * 2^-22 of it, as for every score), ex2 and sums 2^-18, P in two f16 parts 2^-21."""
+    B, grp = 64, 8
+    cache, (q, kn, vn) = _filled([(1, 0)] * B, grp, 1, d, cap, seed=9)
+    cache["sk"].fill_(1.0 / 64)
+    cache["sv"].fill_(1.0 / 64)
+    cache["v8"][:, 8:] = 0
+    vn.zero_()
+    pages = cache["table"][:, 0, 0].long()
+    k = torch.cat([cache["k8"][pages].double() / 64, kn.double()], 1)
+    v = torch.cat([cache["v8"][pages].double() / 64, vn.double()], 1)
+    scale = 1.0 / math.sqrt(d)
+    p = torch.softmax(q.double() @ k.mT * scale, -1)
+    o, mag = p @ v, p @ v.abs()
+    assert int((o.abs() < 0.002 * mag).sum()) > 20
+    out = torch.empty_like(q)
+    tra.paged_attention_decode(cache, q, kn, vn, out, softmax_scale=scale)
+    size = float((q.double().abs() @ k.abs().mT).max()) * scale * 1.4427
+    rel = 2 * size * 2.0 ** -22 * math.log(2) + 2.0 ** -18 + 2.0 ** -21
+    assert bool(((out.double() - o).abs() <= 2.0 ** -8 * o.abs() + rel * mag).all())

@@ -14,9 +14,10 @@
 //               (all within 2^31 of the head's largest), products are exact and summed in fp32:
 //               the scores that the weights are made of lose nothing to quantised queries;
 //   softmax:    lazily rescaled running maximum and sum in fp32, log2 domain;
-//   O += P V:   p in f16 (half a step of 2^-11, random in sign, against the 2^-9 of the bf16
-//               output), transposed between the fragments by movmatrix; the page's V scale is
-//               applied to the fp32 product, so no small scale is lost in f16.
+//   O += P V:   p as a pair of f16, hi + lo (22 bits: f16 alone showed where values cancel), transposed
+//               between the fragments by movmatrix, each with a chain of MMAs of its own (in one
+//               chain: 3 % slower on a ragged batch; the pair itself costs 0 to 1 %); the page's
+//               V scale is applied to the fp32 product, so no small scale is lost in f16.
 // A tail item (up to 64 bf16 rows) is split over the four warps, 16 rows each, straight from
 // global memory with bf16 MMAs; its P goes in as a bf16 pair hi + lo.
 // Every score is written once (fp32, log2 domain) and each piece leaves (m, l, O).
@@ -92,6 +93,7 @@ __device__ __forceinline__ uint32_t pack_h2(float a, float b) {
   const __half2 h = __floats2half2_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
+__device__ __forceinline__ float2 unpack_h2(uint32_t v) { return __half22float2(*reinterpret_cast<const __half2*>(&v)); }
 __device__ __forceinline__ uint32_t pack_b2(float a, float b) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
@@ -450,22 +452,26 @@ __global__ void __launch_bounds__(kStepThreads, 2)
 #pragma unroll
           for (int x = 4; x < 32; x <<= 1) mt[h] = fmaxf(mt[h], __shfl_xor_sync(0xffffffffu, mt[h], x));
         raise(mt);
-        uint32_t pb[NB][2];
+        uint32_t pb[NB][2], pl[NB][2];  // hi, lo
 #pragma unroll
         for (int k = 0; k < NB; ++k) {
           const float p0 = ex2(sr[k][0] - mr[0]), p1 = ex2(sr[k][1] - mr[1]);
           const float p2 = ex2(sr[k][2] - mr[0]), p3 = ex2(sr[k][3] - mr[1]);
           lr[0] += p0 + p2;
           lr[1] += p1 + p3;
-          pb[k][0] = transpose8(pack_h2(p0, p1));
-          pb[k][1] = transpose8(pack_h2(p2, p3));
+          const uint32_t h01 = pack_h2(p0, p1), h23 = pack_h2(p2, p3);
+          const float2 f01 = unpack_h2(h01), f23 = unpack_h2(h23);
+          pb[k][0] = transpose8(h01);
+          pb[k][1] = transpose8(h23);
+          pl[k][0] = transpose8(pack_h2(p0 - f01.x, p1 - f01.y));
+          pl[k][1] = transpose8(pack_h2(p2 - f23.x, p3 - f23.y));
         }
 #pragma unroll
         for (int cb = 0; cb < D / 32; ++cb) {
           const uint32_t off = swz<D>(mrow, 2 * cb + mch);
-          float acc[2][4];
+          float acc[2][4], low[2][4];
 #pragma unroll
-          for (int x = 0; x < 4; ++x) acc[0][x] = acc[1][x] = 0.0f;
+          for (int x = 0; x < 4; ++x) acc[0][x] = acc[1][x] = low[0][x] = low[1][x] = 0.0f;
 #pragma unroll
           for (int k = 0; k < NB; ++k) {
             uint32_t r[4];  // channels 32 cb + 16 h + 2 g4, + 1 of keys 16k + 2 tq, + 1 (, + 8)
@@ -475,12 +481,13 @@ __global__ void __launch_bounds__(kStepThreads, 2)
               const uint32_t u0 = r[2 * h] ^ 0x80808080u, u1 = r[2 * h + 1] ^ 0x80808080u;
               const uint32_t a[4] = {h2_of(u0, 0x4240), h2_of(u0, 0x4341), h2_of(u1, 0x4240), h2_of(u1, 0x4341)};
               mma_f16(acc[h], a, pb[k][0], pb[k][1]);
+              mma_f16(low[h], a, pl[k][0], pl[k][1]);
             }
           }
 #pragma unroll
           for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int x = 0; x < 4; ++x) o[2 * cb + h][x] = fmaf(acc[h][x], sc.y, o[2 * cb + h][x]);
+            for (int x = 0; x < 4; ++x) o[2 * cb + h][x] = fmaf(acc[h][x] + low[h][x], sc.y, o[2 * cb + h][x]);
         }
       };
       for (; ok && next < seen + npage; next += SPLIT ? 1 : kCons) {
