@@ -26,8 +26,8 @@
 // turns the scores into probabilities with the row's m and l, adds them to the weights, writes
 // the output and the new state, and quantises a tail that became full.  The split is what
 // bounds the step: 2 d bytes of codes per cached token, against 4 grp + 8 bytes here.
-// Batch 16 x 32K, 32/8 heads, d 128: split 178 us (6.2 TB/s, 94 % of a copy), step 207 us; a single
-// row of 2K tokens: 9.3 us.
+// On the GPU, batch 16 x 32K, 32/8 heads, d 128: split 176 us (6.2 TB/s, 95 % of a copy), step 208 us;
+// a single row of 2K tokens: 9.6 us.
 #include <cuda_fp16.h>
 
 #include <algorithm>
@@ -802,8 +802,8 @@ cudaError_t launch_step_s(const PagedStepParams& p, const PagedMaps& m, cudaStre
 
 template <int D, int GRP>
 cudaError_t launch_step_g(const PagedStepParams& p, const PagedMaps& m, cudaStream_t s) {
-  // Where the cache has room for few pages per piece the warps split them (a row of 2K tokens: 11.0
-  // -> 9.6 us; 27 pages per piece split or not by a branch in one kernel: 3 % slower than apart).
+  // Where the cache has room for few pages per piece the warps split them (a row of 2K tokens, when
+  // this came in: 11.0 -> 9.3 us; 27 pages per piece split or not by a branch in one kernel: 3 % slower than apart).
   const long long most = (long long)p.c.B * p.c.Hkv * (p.c.cap + 1);
   return most <= (long long)kSplitItems * kPieces ? launch_step_s<D, GRP, true>(p, m, s) : launch_step_s<D, GRP, false>(p, m, s);
 }
