@@ -36,6 +36,26 @@ def test_prompt_importance_on_a_stream(handle):
         del got, other
 
 
+def test_importance_of_a_side_stream_on_the_current_one():
+    """Prompt after prompt on a side stream, each result read on the current stream, late, and dropped: the
+    next one is not written over it."""
+    hq, hkv, d, n = 4, 2, 64, 500
+    gen = _rng(22)
+    q = [_normal(gen, n, hq, d) for _ in range(4)]
+    k, shape, s = _normal(gen, n, hkv, d), tra.Shape([0, n], hq, hkv, d), torch.cuda.Stream()
+    want = [api.prompt_importance(shape, x, k) for x in q]
+    torch.cuda.synchronize()
+    got = []
+    for x in q:
+        w = api.prompt_importance(shape, x, k, stream=s)
+        torch.cuda.current_stream().wait_stream(s)
+        torch.cuda._sleep(10_000_000)
+        got.append(w.clone())
+        del w
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 def test_plan_on_a_stream():
     """A plan used on a stream of its own from its first call on, its weights dropped at once."""
     hq, hkv, d, lens = 8, 2, 128, [500, 200, 64]

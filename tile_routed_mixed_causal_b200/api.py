@@ -158,15 +158,18 @@ def prompt_importance(shape: L.Shape, q, k, n_queries: int = 64, lse=None, scale
     """Accumulated attention weight of the prompt's keys, float32 [ntok, Hkv]: the importance
     that hybrid_select_tokens and paged_cache_fill take.  n_queries: the last queries of each
     sequence that count (0: all); lse: what a prefill wrote, or None to compute it.  The result
-    is made on `stream`, as if that were the current one."""
+    is made on `stream`; the current stream may use it too, once it has waited for that one."""
     scale = 1.0 / math.sqrt(shape.d) if scale is None else scale
     given = lse is not None
+    caller = torch.cuda.current_stream(q.device) if stream is not None and q.is_cuda else None
     with _made_on(stream, q.device):
         weights = torch.empty((shape.ntok, shape.Hkv), dtype=torch.float32, device=q.device)
         if not given:
             lse = torch.empty((shape.Hq, shape.ntok), dtype=torch.float32, device=q.device)
         L.attention_weight_sums(shape, q, k, weights, lse, n_queries=n_queries, softmax_scale=scale,
                                 lse_given=given, stream=stream)
+    if caller is not None:
+        weights.record_stream(caller)   # its memory waits for what the caller's stream does with it
     return weights
 
 
