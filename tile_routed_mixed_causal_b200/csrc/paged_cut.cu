@@ -75,10 +75,11 @@ __device__ __forceinline__ bool cut_fits(const PagedCutParams& p, int4 st) {
   return cut_due(p, st) && st.x <= p.c.cap - p.keep;
 }
 
-// What becomes of row b, for the kernels behind the selection: the CTA beside those of its heads.
+// What becomes of row b, for the kernels behind the selection: the CTA before those of its heads.
 // Where one of the page numbers that the row's pages would be read by and written to is out of
-// range, in any head, the whole row stays.  (Fill of one 8K prompt: 11.3 us without the check, 11.6 so;
-// checked by the selections themselves and joined by the pages' CTAs, 12.1.)
+// range, in any head, the whole row stays.  (Fill of one 8K prompt: 11.3 us with and without the check,
+// 11.6 with this CTA behind the heads', 12.1 checked by the selections themselves and joined by the
+// pages' CTAs.)
 template <bool FILL>
 __device__ __forceinline__ void check_row(const PagedCutParams& p, int b) {
   const tra_paged_cache& c = p.c;
@@ -123,9 +124,9 @@ __global__ void __launch_bounds__(kSelThreads) paged_select_kernel(const PagedCu
   __shared__ uint2 warp_sum[kSpanChunks * 32 + 1];
   __shared__ uint32_t s_bin, s_want;
   grid_release();
-  const int g = blockIdx.x, b = blockIdx.y, t = threadIdx.x, warp = t >> 5, lane = t & 31;
+  const int g = (int)blockIdx.x - 1, b = blockIdx.y, t = threadIdx.x, warp = t >> 5, lane = t & 31;
   const tra_paged_cache& c = p.c;
-  if (g == c.Hkv) {
+  if (g < 0) {
     check_row<FILL>(p, b);
     return;
   }
