@@ -34,7 +34,8 @@
 // to the sum, cancels.  What is left for the exponential, (S - f L) - (1 - f) L, is small where a
 // key has weight, so that the scale's own rounding does not show either.  Sums of 8K to 32K prompts
 // are off by 2e-7 to 7e-7 (an fp32 softmax: 2e-7 to 9e-7), those of 700 tokens with scores up to 155,
-// where single roundings show, by 1.2e-6 at most; the MMA costs 1 % of the time.
+// where single roundings show, by 1.2e-6 at most; the MMA costs 1 to 2 %
+// of the time.
 // Where there are few units a cluster of up to 8 CTAs shares one (every C-th tile each)
 // and joins the partial rows over distributed shared memory in rank order: the same call
 // gives the same bits.
